@@ -439,6 +439,105 @@ int pa_gather_runs(const void* src_k, const void* src_v, int src_blocks,
                    const int32_t* moves, int num_moves,
                    int num_kv_heads, int head_dim, int block_size, int dtype, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * pa_rope  [no counterpart on the pages: rotary positions, applied to the new tokens' q and K
+ *           before the cache write]
+ * For token t at position p = positions[t], every head and pair i = 0 .. rotary_dim/2 - 1, with
+ * (a, b) = elements (i, i + rotary_dim/2) of the head, or (2i, 2i + 1) when `interleaved` != 0:
+ *   (a, b) -> magnitude * (a cos(p f_i) - b sin(p f_i), b cos(p f_i) + a sin(p f_i)),  f_i = inv_freq[i]
+ * Elements rotary_dim .. head_dim-1 are passed on unchanged.  Computed in fp32 and rounded once; the
+ * angle is reduced in 64-bit integers (its error is |p f_i| 2^-52 rad), so that far and negative
+ * positions keep fp32's precision.
+ *   q, k, out_q, out_k: [num_tokens][heads][head_dim] 16-bit elements; a token's heads are contiguous,
+ *     tokens lie *_stride elements apart (a multiple of 8; an input's may be 0).  out_q may be q and
+ *     out_k may be k (same pointer and stride); any other overlap is refused.  num_kv_heads == 0:
+ *     no k (k and out_k are not read).
+ *   positions: int32 (position_bytes 4) or int64 (8) [num_tokens]; inv_freq: double [rotary_dim/2];
+ *     both device memory.
+ * head_dim a multiple of 8 up to 1024, rotary_dim a multiple of 16 up to head_dim.
+ * Returns PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED or PA_ERR_CUDA.
+ * ---------------------------------------------------------------------------------- */
+int pa_rope(void* out_q, void* out_k, const void* q, const void* k, long long out_q_stride, long long out_k_stride,
+            long long q_stride, long long k_stride, const void* positions, int position_bytes, const double* inv_freq,
+            float magnitude, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int rotary_dim,
+            int interleaved, int dtype, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * The 8-bit cache: pools k_cache, v_cache of e4m3 codes [num_blocks][num_kv_heads][block_size][128]
+ * (16-byte aligned) and exponents k_exp, v_exp, int8 [num_blocks][num_kv_heads].  The value of code c
+ * in block b, kv head h is c * 2^e, e = exp[b][h] (read as clamped to -60 .. 60): one power-of-two
+ * scale for each block of tokens and head.  Head size 128, block_size 16/32/64/128.  Whole blocks are
+ * copied by pa_copy_blocks on the pools seen as 16-bit elements of head size 64, with their exponents
+ * copied by the caller.
+ *
+ * pa_cache_append_q8  [P4 §三 sequence diagram; P1 address formula]
+ * Quantise and write each sequence's new rows: sequence s's n_s rows query_start[s] ..
+ * query_start[s+1]-1 of k and v are the tokens at positions L - n_s .. L - 1 of its L = context_lens[s]
+ * (counts clamped and flagged as in pa_multi_query); query_start == NULL: row s is the newest token of
+ * sequence s (num_tokens == num_seqs; sequences with L == 0 write nothing).  In every (block, kv head)
+ * that receives rows, with amax the largest finite |x| of the rows it receives:
+ *   e_need = the least e in -60 .. 60 with amax <= 448 * 2^e (60 when there is none, -60 when amax = 0)
+ *   e      = e_need if offset 0 of the block is among the rows (the block starts afresh),
+ *            else max(e_old, e_need); when e > e_old the block's earlier rows are rounded again from
+ *            their codes, c -> e4m3(c * 2^(e_old - e))
+ *   code   = e4m3(x * 2^-e), to nearest even; +-inf and |x| > 448 * 2^60 become +-448, NaN stays NaN.
+ * Rows of the block behind the new ones are left as they are.  An exponent does not shrink while its
+ * block is appended to.  k, v: 16-bit rows [num_kv_heads][128], tokens k_stride / v_stride elements
+ * apart (multiples of 8).  A block may receive rows of one sequence per call (a shared block is copied
+ * first, as pa_pool_append_token reports): two sequences writing one block leave it unspecified.
+ * A block id outside the pool is not written and sets PA_DEV_BAD_BLOCK_ID.
+ * Returns PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED or PA_ERR_CUDA.
+ * ---------------------------------------------------------------------------------- */
+int pa_cache_append_q8(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache,
+                       void* v_cache, int8_t* k_exp, int8_t* v_exp, const int32_t* block_tables,
+                       const int32_t* context_lens, const int32_t* query_start, int num_seqs, int num_tokens,
+                       int max_q_per_seq, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                       int max_blocks_per_seq, int dtype, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * pa_read_blocks_q8  [P4 §四 whole-block copies, here from the 8-bit pool into a 16-bit one]
+ * For i = 0..num_pairs-1 block dst_ids[i] of the 16-bit pools dst_k, dst_v
+ * ([dst_blocks][num_kv_heads][block_size][128], `dtype`) receives the values c * 2^e of block src_ids[i]
+ * of the 8-bit pools, rounded to nearest (bf16: exact); values beyond fp16's range become its largest.
+ * Whole blocks are read, rows no token has been written to included.  With it pa_multi_query's
+ * prefill tiles serve an 8-bit cache: read the context's blocks back, then prefill over the copy.
+ * A pair with an id outside its pool is skipped and sets PA_DEV_BAD_BLOCK_ID.  Destination blocks must
+ * be distinct.  src_ids, dst_ids: int32 [num_pairs], device memory.
+ * Returns PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED or PA_ERR_CUDA.
+ * ---------------------------------------------------------------------------------- */
+int pa_read_blocks_q8(const void* k_cache, const void* v_cache, const int8_t* k_exp, const int8_t* v_exp,
+                      int src_blocks, void* dst_k, void* dst_v, int dst_blocks, const int32_t* src_ids,
+                      const int32_t* dst_ids, int num_pairs, int num_kv_heads, int head_dim, int block_size, int dtype,
+                      void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * pa_decode_q8 / pa_multi_query_q8  [P4 §五.1; P1 address formula]
+ * pa_decode and pa_multi_query over an 8-bit cache: the same rows, positions, clamping and outputs, with
+ * K[t] and V[t] the values of the cached codes.  Products and sums in fp32, rounded once into `dtype`;
+ * the softmax weights enter the PV product rounded to fp16 (11 bits).  pa_decode_q8: one query row per
+ * sequence, L == 0 gives a zero row.  Rows of q and out that no sequence owns are neither read nor
+ * written.  Tokens of a block whose table entry lies outside the pool are left out of the softmax and set
+ * PA_DEV_BAD_BLOCK_ID (a row with no token left is zero).
+ * Cached rows at positions >= L, and table entries behind them, do not affect the result.
+ * max_q_per_seq x (num_q_heads / num_kv_heads) <= 32 (pa_decode_q8: max_q_per_seq = 1), else
+ * PA_ERR_UNSUPPORTED; longer chunks: pa_read_blocks_q8, then pa_multi_query.
+ * workspace: pa_decode_q8_workspace_size(...) bytes of device memory, 16-byte aligned, caller-owned; its
+ * contents before the call do not matter.  Calls that share a workspace must not overlap on the GPU.
+ * Returns the codes of pa_decode.
+ * ---------------------------------------------------------------------------------- */
+int pa_decode_q8(void* out, const void* q, const void* k_cache, const void* v_cache, const int8_t* k_exp,
+                 const int8_t* v_exp, const int32_t* block_tables, const int32_t* context_lens, float scale,
+                 int num_kv_heads, int num_seqs, int num_q_heads, int head_dim, int block_size, int num_blocks,
+                 int max_blocks_per_seq, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+int pa_multi_query_q8(void* out, const void* q, const void* k_cache, const void* v_cache, const int8_t* k_exp,
+                      const int8_t* v_exp, const int32_t* block_tables, const int32_t* context_lens,
+                      const int32_t* query_start, float scale, int num_kv_heads, int num_seqs, int num_q_tokens,
+                      int max_q_per_seq, int num_q_heads, int head_dim, int block_size, int num_blocks,
+                      int max_blocks_per_seq, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+/* Bytes of workspace the two need for this shape on the current device (0: none, or no such shape). */
+size_t pa_decode_q8_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                   int max_blocks_per_seq, int max_q_per_seq);
+
 /* Bytes of workspace pa_decode needs for this shape on the current device. */
 size_t pa_decode_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                 int block_size, int max_blocks_per_seq);

@@ -12,10 +12,20 @@ as the device-memory and stream provider.
     copy_blocks(src_k, src_v, dst_k, dst_v, src_ids, dst_ids)   # copy-on-write, swap out / in
     BlockPool(num_blocks)                       # host block pool (untimed)
     build_slot_mapping(block_tables, context_lens, block_size)
+
+An 8-bit cache: e4m3 codes [NB, Hkv, B, 128] (torch.float8_e4m3fn) with an int8 exponent per (block, kv head),
+[NB, Hkv], for K and for V; and the rotary positions that come before either cache's write:
+
+    rope(q, k, positions, inv_freq) -> (q, k)
+    cache_append_q8(k, v, k_cache, v_cache, k_exp, v_exp, block_tables, context_lens, query_start=None, max_q=1)
+    decode_q8(q, k_cache, v_cache, k_exp, v_exp, block_tables, context_lens, scale, num_kv_heads) -> out
+    multi_query_q8(q, ..., context_lens, query_start, scale, num_kv_heads, max_q) -> out
+    read_blocks_q8(k_cache, v_cache, k_exp, v_exp, dst_k, dst_v, src_ids, dst_ids)   # back to 16 bits
 """
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Optional
 
 import numpy as np
@@ -27,6 +37,8 @@ from ._native import PAError, DecodeOptions, MATH
 __all__ = ["cache_write", "copy_blocks", "decode", "decode_append", "decode_plan", "decode_plan_runs", "decode_planned", "DecodePlan", "plan_bounds", "plan_rates",
            "planned_workspace_size", "new_planned_workspace",
            "multi_query", "decode_runs", "new_runs_workspace", "gather_runs",
+           "rope_frequencies", "rope", "cache_append_q8", "read_blocks_q8", "decode_q8", "multi_query_q8",
+           "decode_q8_workspace_size",
            "SlotPool", "decode_workspace_size", "plan_tokens_per_split", "kernel_kind",
            "new_workspace", "BlockPool",
            "build_slot_mapping", "read_device_status", "kernel_launch_count", "PAError", "lib"]
@@ -553,6 +565,291 @@ def gather_runs(src_k: torch.Tensor, src_v: torch.Tensor, dst_k: torch.Tensor, d
     rc = lib().pa_gather_runs(src_k.data_ptr(), src_v.data_ptr(), NBs, dst_k.data_ptr(), dst_v.data_ptr(),
                               dst_k.shape[0], moves.data_ptr(), M, H, D, B, _DTYPE[src_k.dtype], _stream_ptr(stream))
     _native.check("pa_gather_runs", rc)
+
+
+# ------------------------------------------------------------------------------------------
+# rotary positions and the 8-bit cache
+# ------------------------------------------------------------------------------------------
+
+def _same_device(stream: Optional[torch.cuda.Stream], first: torch.Tensor, **others) -> torch.device:
+    dev = first.device
+    for n, t in others.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, not on {dev}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, not on {dev}")
+    return dev
+
+
+def _call_on(dev: torch.device, stream: Optional[torch.cuda.Stream], name: str, *args) -> None:
+    """The library call with ``dev`` current, on ``stream`` or dev's current stream."""
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream_ptr(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream_ptr(stream))
+    _native.check(name, rc)
+
+
+def _empty_on(stream: Optional[torch.cuda.Stream], shape, dtype, dev: torch.device) -> torch.Tensor:
+    """Memory allocated for the stream that will use it (so that it is not handed out again early)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _token_rows(name: str, t: torch.Tensor, dtype=None) -> int:
+    """Elements between the tokens of [T, heads, D]; a token's heads must be contiguous (a slice of a
+    projection's output [T, ...] is)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions")
+    T, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0) if T > 1 else H * D
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_context: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """The angles per position (radians, float64 [rotary_dim / 2]) and the magnitude that ``rope`` takes.
+
+    f_i = base^(-2 i / rotary_dim), and for contexts longer than the trained one by ``factor`` (>= 1):
+      "linear"  f_i / factor (positions interpolated);
+      "ntk"     base * factor^(R / (R - 2)) in base's place (the fastest pair stays, the slowest turns
+                factor times slower);
+      "yarn"    f_i for pairs that turn more than ``beta_fast`` times within ``original_context``
+                positions, f_i / factor for those that turn less than ``beta_slow`` times, a linear ramp in
+                i between (its ends rounded outwards to whole pairs), and the magnitude 1 + 0.1 ln(factor)
+                (YaRN, Peng et al. 2023)."""
+    R = int(rotary_dim)
+    if R <= 0 or R % 2 or not base > 1.0 or not factor >= 1.0:
+        raise ValueError("rotary_dim must be even and positive, base above 1, factor at least 1")
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError('scaling must be "none", "linear", "ntk" or "yarn"')
+    magnitude = 1.0
+    if scaling == "ntk":
+        if R <= 2:
+            raise ValueError("ntk scaling needs a rotary_dim above 2")
+        base = base * factor ** (R / (R - 2.0))
+    i = np.arange(R // 2, dtype=np.float64)
+    f = base ** (-2.0 * i / R)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if original_context <= 0 or not beta_fast > beta_slow > 0:
+            raise ValueError("yarn scaling needs original_context and beta_fast > beta_slow > 0")
+
+        def pair_of(turns):   # the (fractional) pair that turns so often within the trained context
+            return R * math.log(original_context / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        lo, hi = max(0, math.floor(pair_of(beta_fast))), min(R - 1, math.ceil(pair_of(beta_slow)))
+        ramp = np.clip((i - lo) / (hi - lo if hi > lo else 0.001), 0.0, 1.0)
+        f = f * (1.0 - ramp) + f / factor * ramp
+        magnitude = 0.1 * math.log(factor) + 1.0
+    return torch.from_numpy(f).to(device), magnitude
+
+
+def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor,
+         magnitude: float = 1.0, interleaved: bool = False, out_q: Optional[torch.Tensor] = None,
+         out_k: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Turn q [T, Hq, D] and k [T, Hkv, D] (or None) by the tokens' positions (int32 or int64 [T]).
+    ``inv_freq``: float64 [R / 2] (see rope_frequencies); the first R elements of each head are turned, as
+    pairs (i, i + R/2) or, ``interleaved``, (2i, 2i + 1).  out_q = q and out_k = k turn them in place.
+    Token strides are free (slices of a fused projection).  Returns (out_q, out_k).  See pa_rope."""
+    qs = _token_rows("q", q)
+    if q.dtype not in _DTYPE:
+        raise TypeError("q must be float16 or bfloat16")
+    T, Hq, D = q.shape
+    ks, Hkv = 0, 0
+    if k is not None:
+        ks = _token_rows("k", k, q.dtype)
+        Hkv = k.shape[1]
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError("k must be [T, Hkv, D] with q's T and D")
+    elif out_k is not None:
+        raise ValueError("out_k without k")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions must be int32 or int64")
+    _need_cuda("positions", positions)
+    _need_cuda("inv_freq", inv_freq, torch.float64)
+    if positions.numel() != T:
+        raise ValueError("positions must have one entry per token")
+    dev = _same_device(stream, q, k=k, positions=positions, inv_freq=inv_freq, out_q=out_q, out_k=out_k)
+    if out_q is None:
+        out_q = _empty_on(stream, q.shape, q.dtype, dev)
+    elif out_q.shape != q.shape:
+        raise ValueError("out_q must have q's shape")
+    oqs, oks = _token_rows("out_q", out_q, q.dtype), 0
+    if k is not None:
+        if out_k is None:
+            out_k = _empty_on(stream, k.shape, k.dtype, dev)
+        elif out_k.shape != k.shape:
+            raise ValueError("out_k must have k's shape")
+        oks = _token_rows("out_k", out_k, k.dtype)
+    _call_on(dev, stream, "pa_rope", out_q.data_ptr(), out_k.data_ptr() if Hkv else None, q.data_ptr(),
+             k.data_ptr() if Hkv else None, oqs, oks, qs, ks, positions.data_ptr(), positions.element_size(),
+             inv_freq.data_ptr(), float(magnitude), T, Hq, Hkv, D, 2 * inv_freq.numel(), int(bool(interleaved)),
+             _DTYPE[q.dtype])
+    return out_q, out_k
+
+
+def _q8_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Tensor, v_exp: torch.Tensor):
+    """Shape (NB, Hkv, B, D) of an 8-bit cache."""
+    _need_cuda("k_cache", k_cache, torch.float8_e4m3fn)
+    _need_cuda("v_cache", v_cache, torch.float8_e4m3fn)
+    _need_cuda("k_exp", k_exp, torch.int8)
+    _need_cuda("v_exp", v_exp, torch.int8)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must be [NB, Hkv, B, D] alike")
+    if k_exp.shape != shape[:2] or v_exp.shape != shape[:2]:
+        raise ValueError("k_exp and v_exp must be [NB, Hkv]")
+    return shape
+
+
+def cache_append_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    k_exp: torch.Tensor, v_exp: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                    query_start: Optional[torch.Tensor] = None, max_q: int = 1,
+                    stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Quantise new rows k, v [T, Hkv, 128] into the slots of their positions: rows query_start[s] ..
+    query_start[s+1]-1 are sequence s's newest tokens (at most ``max_q``), or without query_start row s
+    is sequence s's newest token.  Updates the caches and the exponents of the blocks written.  Token
+    strides of k and v are free.  See pa_cache_append_q8."""
+    NB, Hkv, B, D = _q8_cache(k_cache, v_cache, k_exp, v_exp)
+    ks = _token_rows("k", k)
+    if k.dtype not in _DTYPE:
+        raise TypeError("k must be float16 or bfloat16")
+    vs = _token_rows("v", v, k.dtype)
+    _need_cuda("block_tables", block_tables, torch.int32)
+    _need_cuda("context_lens", context_lens, torch.int32)
+    T = k.shape[0]
+    S = context_lens.numel()
+    if k.shape != (T, Hkv, D) or v.shape != k.shape:
+        raise ValueError("k and v must be [T, Hkv, D] as the cache")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables must be [S, max_blocks] with S = context_lens.numel()")
+    if query_start is not None:
+        _need_cuda("query_start", query_start, torch.int32)
+        if query_start.numel() != S + 1:
+            raise ValueError("query_start must have S + 1 entries")
+    elif T != S:
+        raise ValueError("without query_start, k and v hold one row per sequence")
+    dev = _same_device(stream, k, v=v, k_cache=k_cache, v_cache=v_cache, k_exp=k_exp, v_exp=v_exp,
+                       block_tables=block_tables, context_lens=context_lens, query_start=query_start)
+    _call_on(dev, stream, "pa_cache_append_q8", k.data_ptr(), v.data_ptr(), ks, vs, k_cache.data_ptr(),
+             v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+             query_start.data_ptr() if query_start is not None else None, S, T,
+             int(max_q) if query_start is not None else 1, Hkv, D, B, NB, block_tables.shape[1], _DTYPE[k.dtype])
+
+
+def read_blocks_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Tensor, v_exp: torch.Tensor,
+                   dst_k: torch.Tensor, dst_v: torch.Tensor, src_ids: torch.Tensor, dst_ids: torch.Tensor,
+                   stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Blocks back to 16 bits: dst[dst_ids[i]] = the values of block src_ids[i] (int32 ids; pools dst_k, dst_v
+    [NBd, Hkv, B, 128] float16 or bfloat16).  See pa_read_blocks_q8."""
+    NB, Hkv, B, D = _q8_cache(k_cache, v_cache, k_exp, v_exp)
+    _need_cuda("dst_k", dst_k)
+    if dst_k.dtype not in _DTYPE:
+        raise TypeError("dst_k must be float16 or bfloat16")
+    _need_cuda("dst_v", dst_v, dst_k.dtype)
+    _need_cuda("src_ids", src_ids, torch.int32)
+    _need_cuda("dst_ids", dst_ids, torch.int32)
+    if dst_k.dim() != 4 or dst_k.shape[1:] != k_cache.shape[1:] or dst_v.shape != dst_k.shape:
+        raise ValueError("dst_k and dst_v must be [NBd, Hkv, B, D] as the cache")
+    if src_ids.numel() != dst_ids.numel():
+        raise ValueError("src_ids and dst_ids must have one length")
+    dev = _same_device(stream, k_cache, v_cache=v_cache, k_exp=k_exp, v_exp=v_exp, dst_k=dst_k, dst_v=dst_v,
+                       src_ids=src_ids, dst_ids=dst_ids)
+    _call_on(dev, stream, "pa_read_blocks_q8", k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(),
+             v_exp.data_ptr(), NB, dst_k.data_ptr(), dst_v.data_ptr(), dst_k.shape[0], src_ids.data_ptr(),
+             dst_ids.data_ptr(), src_ids.numel(), Hkv, D, B, _DTYPE[dst_k.dtype])
+
+
+def decode_q8_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
+                             max_blocks_per_seq: int, max_q: int = 1) -> int:
+    return int(lib().pa_decode_q8_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                 max_blocks_per_seq, int(max_q)))
+
+
+def _attention_q8(name, q, k_cache, v_cache, k_exp, v_exp, block_tables, context_lens, query_start, scale,
+                  num_kv_heads, max_q, out, workspace, stream) -> torch.Tensor:
+    _need_cuda("q", q)
+    if q.dtype not in _DTYPE:
+        raise TypeError("q must be float16 or bfloat16")
+    NB, Hkv, B, D = _q8_cache(k_cache, v_cache, k_exp, v_exp)
+    _need_cuda("block_tables", block_tables, torch.int32)
+    _need_cuda("context_lens", context_lens, torch.int32)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    T, Hq, D2 = q.shape
+    S = context_lens.numel()
+    if Hkv != num_kv_heads or D2 != D:
+        raise ValueError("cache shape does not match q / num_kv_heads")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables / context_lens do not match")
+    if query_start is None:
+        if T != S:
+            raise ValueError("q must hold one row per sequence")
+    else:
+        _need_cuda("query_start", query_start, torch.int32)
+        if query_start.numel() != S + 1:
+            raise ValueError("query_start must have S + 1 entries")
+    if out is not None:
+        _need_cuda("out", out, q.dtype)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if workspace is not None:
+        _need_cuda("workspace", workspace)
+    dev = _same_device(stream, q, k_cache=k_cache, v_cache=v_cache, k_exp=k_exp, v_exp=v_exp,
+                       block_tables=block_tables, context_lens=context_lens, query_start=query_start, out=out,
+                       workspace=workspace)
+    max_blocks = block_tables.shape[1]
+    if out is None:
+        out = _empty_on(stream, q.shape, q.dtype, dev)
+    if workspace is None:
+        need = int(lib().pa_decode_q8_workspace_size(S, Hq, Hkv, D, B, max_blocks, max_q))
+        if need:   # of this call alone: its contents before the call do not matter
+            workspace = _empty_on(stream, need, torch.uint8, dev)
+    ws_ptr = workspace.data_ptr() if workspace is not None else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ptrs = (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(),
+            block_tables.data_ptr(), context_lens.data_ptr())
+    if query_start is None:
+        _call_on(dev, stream, name, *ptrs, float(scale), Hkv, S, Hq, D, B, NB, max_blocks, _DTYPE[q.dtype], ws_ptr,
+                 ws_bytes)
+    else:
+        _call_on(dev, stream, name, *ptrs, query_start.data_ptr(), float(scale), Hkv, S, T, max_q, Hq, D, B, NB,
+                 max_blocks, _DTYPE[q.dtype], ws_ptr, ws_bytes)
+    return out
+
+
+def decode_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Tensor,
+              v_exp: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+              num_kv_heads: int, out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Decode attention over an 8-bit cache: q [S, Hq, 128], one query row per sequence; otherwise as
+    ``decode``.  Without ``workspace`` the call allocates its own.  See pa_decode_q8."""
+    return _attention_q8("pa_decode_q8", q, k_cache, v_cache, k_exp, v_exp, block_tables, context_lens, None, scale,
+                         num_kv_heads, 1, out, workspace, stream)
+
+
+def multi_query_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Tensor,
+                   v_exp: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                   query_start: torch.Tensor, scale: float, num_kv_heads: int, max_q: int,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Several new query tokens per sequence over an 8-bit cache, causal, as ``multi_query``;
+    max_q * Hq / Hkv <= 32.  See pa_multi_query_q8."""
+    if query_start is None:
+        raise TypeError("query_start must be a CUDA tensor")
+    return _attention_q8("pa_multi_query_q8", q, k_cache, v_cache, k_exp, v_exp, block_tables, context_lens,
+                         query_start, scale, num_kv_heads, int(max_q), out, workspace, stream)
 
 
 class SlotPool:

@@ -83,6 +83,17 @@ _SIGNATURES = {
     "pa_decode_kernel_kind": (c_int, [c_int, c_int, c_int, ctypes.POINTER(DecodeOptions)]),
     "pa_decode_plan_tokens_per_split": (c_int, [c_int, c_int, c_int, c_int, c_int, c_int,
                                                 ctypes.POINTER(DecodeOptions)]),
+    "pa_rope": (c_int, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_int, c_vp, c_f32, c_int, c_int,
+                        c_int, c_int, c_int, c_int, c_int, c_vp]),
+    "pa_cache_append_q8": (c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_int,
+                                   c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_vp]),
+    "pa_read_blocks_q8": (c_int, [c_vp, c_vp, c_vp, c_vp, c_int, c_vp, c_vp, c_int, c_vp, c_vp, c_int, c_int, c_int,
+                                  c_int, c_int, c_vp]),
+    "pa_decode_q8": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_f32, c_int, c_int, c_int, c_int, c_int,
+                             c_int, c_int, c_int, c_vp, c_size, c_vp]),
+    "pa_multi_query_q8": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_f32, c_int, c_int, c_int,
+                                  c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_vp, c_size, c_vp]),
+    "pa_decode_q8_workspace_size": (c_size, [c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
     "pa_status_string": (ctypes.c_char_p, [c_int]),
     "pa_read_device_status": (c_int, [c_vp, c_int, c_u32p]),
     "pa_kernel_launch_count": (c_u64, []),

@@ -20,9 +20,9 @@ INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = BUILD / "libpa.so"
 
-CUDA_SOURCES = ["api.cu", "cache_write.cu", "copy_blocks.cu", "decode_fma.cu", "decode_mma.cu", "decode_persist.cu", "decode_planned.cu",
-                "decode_static.cu",
-                "prefill_mma.cu", "prefill_tc.cu"]
+CUDA_SOURCES = ["api.cu", "api_q8.cu", "cache_q8.cu", "cache_write.cu", "copy_blocks.cu", "decode_fma.cu", "decode_mma.cu",
+                "decode_persist.cu", "decode_planned.cu", "decode_q8.cu", "decode_static.cu",
+                "prefill_mma.cu", "prefill_tc.cu", "rope.cu"]
 CXX_SOURCES = ["pool.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

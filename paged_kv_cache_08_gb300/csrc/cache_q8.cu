@@ -1,0 +1,229 @@
+// The 8-bit cache's write and read-back.
+//
+// append_q8: each sequence's new rows go to the slots of their positions ("显存虚拟化革命：PagedAttention
+// 内存池管理与显存碎片终结", §三 sequence diagram; the address rule of "端侧 SLM 显存保活术：在 4GB
+// 内存板卡上实现轻量 PagedAttention 与 KV 缓存分块"), quantised with one exponent per (block, kv head):
+//   e_need = least e with amax <= 448 * 2^e, amax over the finite |x| of the call's rows in the block
+//   e      = e_need                  when the call writes the block's offset 0 (the block starts afresh)
+//          = max(e_old, e_need)      otherwise; rows before the new ones are rounded again if e grew
+//   code   = e4m3(x * 2^-e)          to nearest even; beyond 448 (inf, or amax > 448 * 2^60) to +-448
+// The products by a power of two are exact, so a code is off by its own rounding alone.
+//
+// Design: one unit of B / 16 warps per (touched block, kv head, K or V): it alone decides the block's
+// exponent, so there are no atomics and the result has one value.  A warp holds its 16 rows in
+// registers (one pass over the new rows).  The host does not know how many blocks a ragged batch
+// touches; unit v of a sequence is found by a search in the monotone bounds
+// query_start[s] / B + 2 s, which leave every sequence at least the blocks it touches.
+//
+// read_q8: code * 2^e rounded to the pool's 16-bit type (bf16 exactly), beyond its range to its
+// largest value; one thread per 16 codes of K and of V.  Both are bound by HBM.
+#include "q8.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kAppendWarps = 8;
+
+// Largest s in [0, S) with q_start[s] / B + 2 s <= v, by the lanes of a warp together.
+__device__ __forceinline__ int find_seq(const AppendQ8Args& a, int v, int lane) {
+    int lo = 0, hi = a.num_seqs;   // the answer lies in [lo, hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int s = lo + lane * step;
+        const bool le = s < hi && max(0, min(a.q_start[s], a.rows)) / a.block_size + 2LL * s <= v;
+        const unsigned m = __ballot_sync(0xffffffffu, le);
+        const int k = m ? 31 - __clz(m) : 0;
+        lo = lo + k * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
+// |x| where x is finite, else 0
+__device__ __forceinline__ float finite_abs(float x) {
+    const float f = fabsf(x);
+    return f <= 3.402823466e38f ? f : 0.f;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAppendWarps * 32) append_q8_kernel(const AppendQ8Args a, int units) {
+    __shared__ float amax_of[kAppendWarps];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int B = a.block_size, Hkv = a.num_kv_heads;
+    const int wpu = B / 16;                                    // warps per unit
+    const long long u = (long long)blockIdx.x * (kAppendWarps / wpu) + warp / wpu;
+    const int part = warp % wpu;                               // 16-row part of the block
+    // unit -> (virtual block, head, K or V)
+    const int is_v = (int)(u % 2);
+    const int h = (int)(u / 2 % Hkv);
+    const long long v = u / 2 / Hkv;
+    bool live = v < units;
+    int s = 0, j = 0, L = 0;
+    NewRows nr{0, 0, false};
+    if (live) {
+        if (a.q_start) {
+            s = find_seq(a, (int)v, lane);
+            j = (int)(v - (max(0, min(a.q_start[s], a.rows)) / B + 2LL * s));
+        } else {
+            s = (int)v;
+        }
+        bool bad_len;
+        L = clamped_len(a.context_lens, s, a.max_blocks_per_seq, B, &bad_len);
+        nr = new_rows(a.q_start, a.rows, a.max_q, s, L);
+        if ((bad_len || nr.bad) && j == 0 && h == 0 && !is_v && part == 0 && lane == 0)
+            flag_status(a.status, PA_DEV_BAD_CONTEXT);
+    }
+    const int p0 = L - nr.n;                                   // first new position
+    const int blk_i = p0 / B + j;                              // logical block
+    live = live && j >= 0 && nr.n > 0 && blk_i <= (L - 1) / B;
+    int blk = -1, lo = 0, hi = 0;
+    if (live) {
+        blk = a.block_tables[(size_t)s * a.max_blocks_per_seq + blk_i];
+        lo = max(0, p0 - blk_i * B);                           // new rows of the block: [lo, hi)
+        hi = min(B, L - blk_i * B);
+        if (blk < 0 || blk >= a.num_blocks) {
+            if (h == 0 && !is_v && part == 0 && lane == 0) flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+            live = false;
+        }
+    }
+    // this warp's rows: part * 16 + 2 i + lane / 16, eight elements (lane % 16) of each
+    const int r0 = part * 16 + lane / 16, c = lane % 16;
+    uint4 x[8];
+    float amax = 0.f;
+    const T* src = nullptr;
+    if (live) {
+        const long long stride = is_v ? a.v_stride : a.k_stride;
+        src = static_cast<const T*>(is_v ? a.v : a.k) + (nr.row0 + (long long)(blk_i * B - p0)) * stride + h * kHeadDim +
+              c * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + 2 * i;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r >= lo && r < hi) x[i] = __ldg(reinterpret_cast<const uint4*>(src + r * stride));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float f[8];
+            unpack8<T>(x[i], f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) amax = fmaxf(amax, finite_abs(f[k]));
+        }
+    }
+    amax = warp_max(amax);
+    const size_t tile = (size_t)(live ? blk : 0) * Hkv + h;
+    int8_t* exps = is_v ? a.v_exp : a.k_exp;
+    const int e_old = live ? clamp_exp(exps[tile]) : 0;
+    if (wpu > 1) {
+        if (lane == 0) amax_of[warp] = amax;
+        __syncthreads();
+        for (int i = warp - part; i < warp - part + wpu; ++i) amax = fmaxf(amax, amax_of[i]);
+    } else {
+        __syncwarp();
+    }
+    if (!live) return;
+    const int need = exponent_for(amax);
+    const int e = lo == 0 ? need : max(e_old, need);
+    uint8_t* dst = (is_v ? a.v_cache : a.k_cache) + tile * B * kHeadDim + c * 8;
+    const float mul = exp2_int(-e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + 2 * i;
+        if (r >= lo && r < hi) {
+            float f[8];
+            unpack8<T>(x[i], f);
+            uint32_t w[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                w[k] = (uint32_t)f32_to_e4m3x2(f[4 * k] * mul, f[4 * k + 1] * mul) |
+                       ((uint32_t)f32_to_e4m3x2(f[4 * k + 2] * mul, f[4 * k + 3] * mul) << 16);
+            *reinterpret_cast<uint2*>(dst + r * kHeadDim) = make_uint2(w[0], w[1]);
+        } else if (r < lo && e > e_old) {
+            // an earlier row: the same values under the grown exponent
+            const uint2 old = *reinterpret_cast<const uint2*>(dst + r * kHeadDim);
+            const uint32_t o[2] = {old.x, old.y};
+            const float down = exp2_int(e_old - e);
+            uint32_t w[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float2 p = e4m3x2_to_float2((uint16_t)(o[k] & 0xffffu));
+                const float2 q = e4m3x2_to_float2((uint16_t)(o[k] >> 16));
+                w[k] = (uint32_t)f32_to_e4m3x2(p.x * down, p.y * down) |
+                       ((uint32_t)f32_to_e4m3x2(q.x * down, q.y * down) << 16);
+            }
+            *reinterpret_cast<uint2*>(dst + r * kHeadDim) = make_uint2(w[0], w[1]);
+        }
+    }
+    if (part == 0 && lane == 0) exps[tile] = (int8_t)e;
+}
+
+// Two fp32 to two 16-bit values, to nearest; beyond the type's range to its largest value, NaN stays.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2_sat(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2_sat<__half>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2_sat<__nv_bfloat16>(float lo, float hi) {
+    return Elem<__nv_bfloat16>::pack2(lo, hi);   // 448 * 2^60 is far inside bf16's range
+}
+
+template <typename T>
+__device__ __forceinline__ void read16(uint4 codes, float mul, uint4* dst) {
+    const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = e4m3x2_to_float2((uint16_t)(c[i] & 0xffffu));
+        const float2 q = e4m3x2_to_float2((uint16_t)(c[i] >> 16));
+        w[2 * i] = pack2_sat<T>(p.x * mul, p.y * mul);
+        w[2 * i + 1] = pack2_sat<T>(q.x * mul, q.y * mul);
+    }
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) read_q8_kernel(const ReadQ8Args a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const int per_block = a.num_kv_heads * a.vecs_per_head;
+    const long long pair = i / per_block;
+    if (pair >= a.num_pairs) return;
+    const int v = (int)(i - pair * per_block);
+    const int src = a.src_ids[pair], dst = a.dst_ids[pair];
+    if (src < 0 || src >= a.src_blocks || dst < 0 || dst >= a.dst_blocks) {
+        if (v == 0) flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+        return;
+    }
+    const size_t tile = (size_t)src * a.num_kv_heads + v / a.vecs_per_head;
+    const size_t from = (size_t)src * per_block + v, to = ((size_t)dst * per_block + v) * 2;
+    read16<T>(a.k_cache[from], exp2_int(clamp_exp(a.k_exp[tile])), a.dst_k + to);
+    read16<T>(a.v_cache[from], exp2_int(clamp_exp(a.v_exp[tile])), a.dst_v + to);
+}
+
+}  // namespace
+
+cudaError_t launch_append_q8(const AppendQ8Args& a, int dtype, cudaStream_t stream) {
+    const int units = a.q_start ? a.rows / a.block_size + 2 * a.num_seqs : a.num_seqs;
+    const long long all = 2LL * units * a.num_kv_heads;
+    const int per_cta = kAppendWarps / (a.block_size / 16);
+    const dim3 grid((unsigned)((all + per_cta - 1) / per_cta)), block(kAppendWarps * 32);
+    return dtype == PA_BF16 ? launch_pdl(append_q8_kernel<__nv_bfloat16>, grid, block, 0, stream, a, units)
+                            : launch_pdl(append_q8_kernel<__half>, grid, block, 0, stream, a, units);
+}
+
+cudaError_t launch_read_q8(const ReadQ8Args& a, int dtype, cudaStream_t stream) {
+    const long long vecs = (long long)a.num_pairs * a.num_kv_heads * a.vecs_per_head;
+    const dim3 grid((unsigned)((vecs + 255) / 256)), block(256);
+    return dtype == PA_BF16 ? launch_pdl(read_q8_kernel<__nv_bfloat16>, grid, block, 0, stream, a)
+                            : launch_pdl(read_q8_kernel<__half>, grid, block, 0, stream, a);
+}
+
+}  // namespace pa
