@@ -191,6 +191,7 @@ static int q8_attention_shape(int num_seqs, int num_q_heads, int num_kv_heads, i
     if (rc != PA_OK) return rc;
     if (num_q_heads <= 0 || num_q_heads % num_kv_heads || max_q < 1) return PA_ERR_INVALID_ARG;
     if (num_q_heads > 65535 || (long long)(num_q_heads / num_kv_heads) * max_q > kQ8MaxRows) return PA_ERR_UNSUPPORTED;
+    if (!q8_line_fits(num_seqs, num_kv_heads, block_size, max_blocks_per_seq)) return PA_ERR_UNSUPPORTED;
     return PA_OK;
 }
 

@@ -40,12 +40,6 @@ __device__ __forceinline__ int find_seq(const AppendQ8Args& a, int v, int lane) 
     return lo;
 }
 
-// |x| where x is finite, else 0
-__device__ __forceinline__ float finite_abs(float x) {
-    const float f = fabsf(x);
-    return f <= 3.402823466e38f ? f : 0.f;
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_q8_kernel(const AppendQ8Args a, int units) {
     __shared__ float amax_of[kAppendWarps];

@@ -8,6 +8,8 @@
 // every code that stays normal, and every kernel applies the scale by adding an exponent.
 #pragma once
 
+#include <utility>
+
 #include "pa_internal.cuh"
 
 namespace pa {
@@ -113,6 +115,12 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t c) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// |x| where x is finite, else 0
+__device__ __forceinline__ float finite_abs(float x) {
+    const float f = fabsf(x);
+    return f <= 3.402823466e38f ? f : 0.f;
+}
+
 __device__ __forceinline__ int clamp_exp(int e) { return max(kExpMin, min(kExpMax, e)); }
 
 // 2^e, -126 <= e <= 127
@@ -155,6 +163,7 @@ cudaError_t launch_append_q8(const AppendQ8Args& a, int dtype, cudaStream_t stre
 cudaError_t launch_read_q8(const ReadQ8Args& a, int dtype, cudaStream_t stream);
 size_t q8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int max_q, int block_size,
                           int max_blocks_per_seq);
+bool q8_line_fits(int num_seqs, int num_kv_heads, int block_size, int max_blocks_per_seq);
 cudaError_t launch_decode_q8(const DecodeQ8Args& a, int dtype, void* workspace, cudaStream_t stream);
 
 // Launch with programmatic serialisation: the kernel may start its prologue while the preceding
