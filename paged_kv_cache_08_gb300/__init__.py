@@ -25,6 +25,7 @@ An 8-bit cache: e4m3 codes [NB, Hkv, B, 128] (torch.float8_e4m3fn) with an int8 
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional
 
@@ -571,48 +572,81 @@ def gather_runs(src_k: torch.Tensor, src_v: torch.Tensor, dst_k: torch.Tensor, d
 # rotary positions and the 8-bit cache
 # ------------------------------------------------------------------------------------------
 
-def _same_device(stream: Optional[torch.cuda.Stream], first: torch.Tensor, **others) -> torch.device:
-    dev = first.device
-    for n, t in others.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{n} is on {t.device}, not on {dev}")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, not on {dev}")
-    return dev
+# These calls are short on the GPU (microseconds), so their checks touch each tensor once: its type, device
+# and layout together, with the message worked out only when one is wrong.
+
+def _want(name: str, t, dtype, dev: int) -> int:
+    """The address of a contiguous tensor of ``dtype`` on CUDA device ``dev``."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need_cuda(name, t, dtype)
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
 
 
-def _call_on(dev: torch.device, stream: Optional[torch.cuda.Stream], name: str, *args) -> None:
-    """The library call with ``dev`` current, on ``stream`` or dev's current stream."""
-    fn = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _stream_ptr(stream))
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _stream_ptr(stream))
-    _native.check(name, rc)
-
-
-def _empty_on(stream: Optional[torch.cuda.Stream], shape, dtype, dev: torch.device) -> torch.Tensor:
-    """Memory allocated for the stream that will use it (so that it is not handed out again early)."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-
-def _token_rows(name: str, t: torch.Tensor, dtype=None) -> int:
-    """Elements between the tokens of [T, heads, D]; a token's heads must be contiguous (a slice of a
-    projection's output [T, ...] is)."""
+def _want_rows(name: str, t, dtype, dev: int, shape=None):
+    """Address, and elements between the tokens, of [T, heads, D] with a token's heads contiguous (a slice of
+    a projection's output is)."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.dim() == 3 and (shape is None or t.shape == shape):
+            T, H, D = t.shape
+            if t.is_contiguous():
+                return t.data_ptr(), H * D
+            st, sh, sd = t.stride()
+            if (D == 1 or sd == 1) and (H == 1 or sh == D):
+                return t.data_ptr(), st if T > 1 else H * D
+            raise ValueError(f"the heads of a token of {name} must be contiguous")
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have three dimensions")
-    T, H, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
-        raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0) if T > 1 else H * D
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    raise ValueError(f"{name} must be [T, heads, D], got {tuple(t.shape)}" if shape is None else
+                     f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _device_and_type(name: str, t):
+    """CUDA device index and library type of a 16-bit operand."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    dt = _DTYPE.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float16 or bfloat16")
+    return t.get_device(), dt
+
+
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call_on(dev: int, stream: Optional[torch.cuda.Stream], name: str, *args) -> None:
+    """The library call with device ``dev`` current, on ``stream`` or dev's current stream."""
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"stream is on {stream.device}, not on cuda:{dev}")
+        raw = stream.cuda_stream
+    else:
+        raw = _current_raw_stream(dev) if _current_raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    fn = getattr(_native.load(), name)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, raw)
+    if rc < 0:
+        raise PAError(name, rc)
+
+
+def _empty_on(stream: Optional[torch.cuda.Stream], shape, dtype, device) -> torch.Tensor:
+    """Memory allocated for the stream that will use it (so that it is not handed out again early)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -662,55 +696,51 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, in
     ``inv_freq``: float64 [R / 2] (see rope_frequencies); the first R elements of each head are turned, as
     pairs (i, i + R/2) or, ``interleaved``, (2i, 2i + 1).  out_q = q and out_k = k turn them in place.
     Token strides are free (slices of a fused projection).  Returns (out_q, out_k).  See pa_rope."""
-    qs = _token_rows("q", q)
-    if q.dtype not in _DTYPE:
-        raise TypeError("q must be float16 or bfloat16")
+    dev, dt = _device_and_type("q", q)
+    q_ptr, qs = _want_rows("q", q, q.dtype, dev)
     T, Hq, D = q.shape
-    ks, Hkv = 0, 0
+    k_ptr, ks, Hkv = None, 0, 0
     if k is not None:
-        ks = _token_rows("k", k, q.dtype)
+        k_ptr, ks = _want_rows("k", k, q.dtype, dev)
         Hkv = k.shape[1]
-        if k.shape[0] != T or k.shape[2] != D:
+        if k.shape[0] != T or k.shape[2] != D or Hkv == 0:
             raise ValueError("k must be [T, Hkv, D] with q's T and D")
     elif out_k is not None:
         raise ValueError("out_k without k")
-    if positions.dtype not in (torch.int32, torch.int64):
-        raise TypeError("positions must be int32 or int64")
-    _need_cuda("positions", positions)
-    _need_cuda("inv_freq", inv_freq, torch.float64)
+    wide = isinstance(positions, torch.Tensor) and positions.dtype is torch.int64
+    if not wide and not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32):
+        raise TypeError("positions must be an int32 or int64 tensor")
+    p_ptr = _want("positions", positions, positions.dtype, dev)
+    f_ptr = _want("inv_freq", inv_freq, torch.float64, dev)
     if positions.numel() != T:
         raise ValueError("positions must have one entry per token")
-    dev = _same_device(stream, q, k=k, positions=positions, inv_freq=inv_freq, out_q=out_q, out_k=out_k)
     if out_q is None:
-        out_q = _empty_on(stream, q.shape, q.dtype, dev)
-    elif out_q.shape != q.shape:
-        raise ValueError("out_q must have q's shape")
-    oqs, oks = _token_rows("out_q", out_q, q.dtype), 0
+        out_q = _empty_on(stream, (T, Hq, D), q.dtype, q.device)
+        oq_ptr, oqs = out_q.data_ptr(), Hq * D
+    else:
+        oq_ptr, oqs = _want_rows("out_q", out_q, q.dtype, dev, q.shape)
+    ok_ptr, oks = None, 0
     if k is not None:
         if out_k is None:
-            out_k = _empty_on(stream, k.shape, k.dtype, dev)
-        elif out_k.shape != k.shape:
-            raise ValueError("out_k must have k's shape")
-        oks = _token_rows("out_k", out_k, k.dtype)
-    _call_on(dev, stream, "pa_rope", out_q.data_ptr(), out_k.data_ptr() if Hkv else None, q.data_ptr(),
-             k.data_ptr() if Hkv else None, oqs, oks, qs, ks, positions.data_ptr(), positions.element_size(),
-             inv_freq.data_ptr(), float(magnitude), T, Hq, Hkv, D, 2 * inv_freq.numel(), int(bool(interleaved)),
-             _DTYPE[q.dtype])
+            out_k = _empty_on(stream, (T, Hkv, D), q.dtype, q.device)
+            ok_ptr, oks = out_k.data_ptr(), Hkv * D
+        else:
+            ok_ptr, oks = _want_rows("out_k", out_k, q.dtype, dev, k.shape)
+    _call_on(dev, stream, "pa_rope", oq_ptr, ok_ptr, q_ptr, k_ptr, oqs, oks, qs, ks, p_ptr, 8 if wide else 4, f_ptr,
+             float(magnitude), T, Hq, Hkv, D, 2 * inv_freq.numel(), 1 if interleaved else 0, dt)
     return out_q, out_k
 
 
-def _q8_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Tensor, v_exp: torch.Tensor):
-    """Shape (NB, Hkv, B, D) of an 8-bit cache."""
-    _need_cuda("k_cache", k_cache, torch.float8_e4m3fn)
-    _need_cuda("v_cache", v_cache, torch.float8_e4m3fn)
-    _need_cuda("k_exp", k_exp, torch.int8)
-    _need_cuda("v_exp", v_exp, torch.int8)
+def _q8_cache(k_cache, v_cache, k_exp, v_exp, dev: int):
+    """Shape (NB, Hkv, B, D) and the four addresses of an 8-bit cache."""
+    ptrs = (_want("k_cache", k_cache, torch.float8_e4m3fn, dev), _want("v_cache", v_cache, torch.float8_e4m3fn, dev),
+            _want("k_exp", k_exp, torch.int8, dev), _want("v_exp", v_exp, torch.int8, dev))
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [NB, Hkv, B, D] alike")
-    if k_exp.shape != shape[:2] or v_exp.shape != shape[:2]:
+    if k_exp.shape != shape[:2] or v_exp.shape != k_exp.shape:
         raise ValueError("k_exp and v_exp must be [NB, Hkv]")
-    return shape
+    return shape, ptrs
 
 
 def cache_append_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -721,31 +751,27 @@ def cache_append_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     query_start[s+1]-1 are sequence s's newest tokens (at most ``max_q``), or without query_start row s
     is sequence s's newest token.  Updates the caches and the exponents of the blocks written.  Token
     strides of k and v are free.  See pa_cache_append_q8."""
-    NB, Hkv, B, D = _q8_cache(k_cache, v_cache, k_exp, v_exp)
-    ks = _token_rows("k", k)
-    if k.dtype not in _DTYPE:
-        raise TypeError("k must be float16 or bfloat16")
-    vs = _token_rows("v", v, k.dtype)
-    _need_cuda("block_tables", block_tables, torch.int32)
-    _need_cuda("context_lens", context_lens, torch.int32)
-    T = k.shape[0]
+    dev, dt = _device_and_type("k", k)
+    (NB, Hkv, B, D), cache = _q8_cache(k_cache, v_cache, k_exp, v_exp, dev)
+    k_ptr, ks = _want_rows("k", k, k.dtype, dev)
+    v_ptr, vs = _want_rows("v", v, k.dtype, dev, k.shape)
+    bt_ptr = _want("block_tables", block_tables, torch.int32, dev)
+    cl_ptr = _want("context_lens", context_lens, torch.int32, dev)
+    T, H2, D2 = k.shape
     S = context_lens.numel()
-    if k.shape != (T, Hkv, D) or v.shape != k.shape:
+    if H2 != Hkv or D2 != D:
         raise ValueError("k and v must be [T, Hkv, D] as the cache")
     if block_tables.dim() != 2 or block_tables.shape[0] != S:
         raise ValueError("block_tables must be [S, max_blocks] with S = context_lens.numel()")
+    qs_ptr = None
     if query_start is not None:
-        _need_cuda("query_start", query_start, torch.int32)
+        qs_ptr = _want("query_start", query_start, torch.int32, dev)
         if query_start.numel() != S + 1:
             raise ValueError("query_start must have S + 1 entries")
     elif T != S:
         raise ValueError("without query_start, k and v hold one row per sequence")
-    dev = _same_device(stream, k, v=v, k_cache=k_cache, v_cache=v_cache, k_exp=k_exp, v_exp=v_exp,
-                       block_tables=block_tables, context_lens=context_lens, query_start=query_start)
-    _call_on(dev, stream, "pa_cache_append_q8", k.data_ptr(), v.data_ptr(), ks, vs, k_cache.data_ptr(),
-             v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
-             query_start.data_ptr() if query_start is not None else None, S, T,
-             int(max_q) if query_start is not None else 1, Hkv, D, B, NB, block_tables.shape[1], _DTYPE[k.dtype])
+    _call_on(dev, stream, "pa_cache_append_q8", k_ptr, v_ptr, ks, vs, *cache, bt_ptr, cl_ptr, qs_ptr, S, T,
+             int(max_q) if qs_ptr is not None else 1, Hkv, D, B, NB, block_tables.shape[1], dt)
 
 
 def read_blocks_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Tensor, v_exp: torch.Tensor,
@@ -753,22 +779,19 @@ def read_blocks_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Te
                    stream: Optional[torch.cuda.Stream] = None) -> None:
     """Blocks back to 16 bits: dst[dst_ids[i]] = the values of block src_ids[i] (int32 ids; pools dst_k, dst_v
     [NBd, Hkv, B, 128] float16 or bfloat16).  See pa_read_blocks_q8."""
-    NB, Hkv, B, D = _q8_cache(k_cache, v_cache, k_exp, v_exp)
-    _need_cuda("dst_k", dst_k)
-    if dst_k.dtype not in _DTYPE:
-        raise TypeError("dst_k must be float16 or bfloat16")
-    _need_cuda("dst_v", dst_v, dst_k.dtype)
-    _need_cuda("src_ids", src_ids, torch.int32)
-    _need_cuda("dst_ids", dst_ids, torch.int32)
-    if dst_k.dim() != 4 or dst_k.shape[1:] != k_cache.shape[1:] or dst_v.shape != dst_k.shape:
+    dev, dt = _device_and_type("dst_k", dst_k)
+    (NB, Hkv, B, D), cache = _q8_cache(k_cache, v_cache, k_exp, v_exp, dev)
+    dk_ptr = _want("dst_k", dst_k, dst_k.dtype, dev)
+    dv_ptr = _want("dst_v", dst_v, dst_k.dtype, dev)
+    src_ptr = _want("src_ids", src_ids, torch.int32, dev)
+    dst_ptr = _want("dst_ids", dst_ids, torch.int32, dev)
+    shape = dst_k.shape
+    if len(shape) != 4 or shape[1:] != k_cache.shape[1:] or dst_v.shape != shape:
         raise ValueError("dst_k and dst_v must be [NBd, Hkv, B, D] as the cache")
-    if src_ids.numel() != dst_ids.numel():
+    n = src_ids.numel()
+    if dst_ids.numel() != n:
         raise ValueError("src_ids and dst_ids must have one length")
-    dev = _same_device(stream, k_cache, v_cache=v_cache, k_exp=k_exp, v_exp=v_exp, dst_k=dst_k, dst_v=dst_v,
-                       src_ids=src_ids, dst_ids=dst_ids)
-    _call_on(dev, stream, "pa_read_blocks_q8", k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(),
-             v_exp.data_ptr(), NB, dst_k.data_ptr(), dst_v.data_ptr(), dst_k.shape[0], src_ids.data_ptr(),
-             dst_ids.data_ptr(), src_ids.numel(), Hkv, D, B, _DTYPE[dst_k.dtype])
+    _call_on(dev, stream, "pa_read_blocks_q8", *cache, NB, dk_ptr, dv_ptr, shape[0], src_ptr, dst_ptr, n, Hkv, D, B, dt)
 
 
 def decode_q8_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
@@ -777,14 +800,19 @@ def decode_q8_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
                                                  max_blocks_per_seq, int(max_q)))
 
 
+@functools.lru_cache(maxsize=256)
+def _q8_workspace_size(dev: int, *shape) -> int:
+    with torch.cuda.device(dev):
+        return decode_q8_workspace_size(*shape)
+
+
 def _attention_q8(name, q, k_cache, v_cache, k_exp, v_exp, block_tables, context_lens, query_start, scale,
                   num_kv_heads, max_q, out, workspace, stream) -> torch.Tensor:
-    _need_cuda("q", q)
-    if q.dtype not in _DTYPE:
-        raise TypeError("q must be float16 or bfloat16")
-    NB, Hkv, B, D = _q8_cache(k_cache, v_cache, k_exp, v_exp)
-    _need_cuda("block_tables", block_tables, torch.int32)
-    _need_cuda("context_lens", context_lens, torch.int32)
+    dev, dt = _device_and_type("q", q)
+    q_ptr = _want("q", q, q.dtype, dev)
+    (NB, Hkv, B, D), cache = _q8_cache(k_cache, v_cache, k_exp, v_exp, dev)
+    bt_ptr = _want("block_tables", block_tables, torch.int32, dev)
+    cl_ptr = _want("context_lens", context_lens, torch.int32, dev)
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, D]")
     T, Hq, D2 = q.shape
@@ -793,39 +821,36 @@ def _attention_q8(name, q, k_cache, v_cache, k_exp, v_exp, block_tables, context
         raise ValueError("cache shape does not match q / num_kv_heads")
     if block_tables.dim() != 2 or block_tables.shape[0] != S:
         raise ValueError("block_tables / context_lens do not match")
-    if query_start is None:
-        if T != S:
-            raise ValueError("q must hold one row per sequence")
-    else:
-        _need_cuda("query_start", query_start, torch.int32)
+    max_blocks = block_tables.shape[1]
+    qs_ptr = None
+    if query_start is not None:
+        qs_ptr = _want("query_start", query_start, torch.int32, dev)
         if query_start.numel() != S + 1:
             raise ValueError("query_start must have S + 1 entries")
-    if out is not None:
-        _need_cuda("out", out, q.dtype)
+    elif T != S:
+        raise ValueError("q must hold one row per sequence")
+    if out is None:
+        out = _empty_on(stream, (T, Hq, D), q.dtype, q.device)
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _want("out", out, q.dtype, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
+    ws_ptr, ws_bytes = None, 0
     if workspace is not None:
-        _need_cuda("workspace", workspace)
-    dev = _same_device(stream, q, k_cache=k_cache, v_cache=v_cache, k_exp=k_exp, v_exp=v_exp,
-                       block_tables=block_tables, context_lens=context_lens, query_start=query_start, out=out,
-                       workspace=workspace)
-    max_blocks = block_tables.shape[1]
-    if out is None:
-        out = _empty_on(stream, q.shape, q.dtype, dev)
-    if workspace is None:
-        need = int(lib().pa_decode_q8_workspace_size(S, Hq, Hkv, D, B, max_blocks, max_q))
-        if need:   # of this call alone: its contents before the call do not matter
-            workspace = _empty_on(stream, need, torch.uint8, dev)
-    ws_ptr = workspace.data_ptr() if workspace is not None else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    ptrs = (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(),
-            block_tables.data_ptr(), context_lens.data_ptr())
-    if query_start is None:
-        _call_on(dev, stream, name, *ptrs, float(scale), Hkv, S, Hq, D, B, NB, max_blocks, _DTYPE[q.dtype], ws_ptr,
-                 ws_bytes)
+        ws_ptr = _want("workspace", workspace, workspace.dtype, dev)
+        ws_bytes = workspace.numel() * workspace.element_size()
     else:
-        _call_on(dev, stream, name, *ptrs, query_start.data_ptr(), float(scale), Hkv, S, T, max_q, Hq, D, B, NB,
-                 max_blocks, _DTYPE[q.dtype], ws_ptr, ws_bytes)
+        ws_bytes = _q8_workspace_size(dev, S, Hq, Hkv, D, B, max_blocks, max_q)
+        if ws_bytes:   # of this call alone: its contents before the call do not matter
+            workspace = _empty_on(stream, (ws_bytes,), torch.uint8, q.device)
+            ws_ptr = workspace.data_ptr()
+    if qs_ptr is None:
+        _call_on(dev, stream, name, out_ptr, q_ptr, *cache, bt_ptr, cl_ptr, float(scale), Hkv, S, Hq, D, B, NB, max_blocks,
+                 dt, ws_ptr, ws_bytes)
+    else:
+        _call_on(dev, stream, name, out_ptr, q_ptr, *cache, bt_ptr, cl_ptr, qs_ptr, float(scale), Hkv, S, T, max_q, Hq, D,
+                 B, NB, max_blocks, dt, ws_ptr, ws_bytes)
     return out
 
 

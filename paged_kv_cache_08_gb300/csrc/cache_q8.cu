@@ -9,14 +9,16 @@
 //   code   = e4m3(x * 2^-e)          to nearest even; beyond 448 (inf, or amax > 448 * 2^60) to +-448
 // The products by a power of two are exact, so a code is off by its own rounding alone.
 //
-// Design: one unit of B / 16 warps per (touched block, kv head, K or V): it alone decides the block's
-// exponent, so there are no atomics and the result has one value.  A warp holds its 16 rows in
-// registers (one pass over the new rows).  The host does not know how many blocks a ragged batch
-// touches; unit v of a sequence is found by a search in the monotone bounds
+// Design: one warp per (touched block, kv head, K or V): it alone decides the block's exponent, so there are
+// no atomics and the result has one value.  It holds 16 rows in registers (32 where a block has 32) and
+// reads those before them again, from L2, once the exponent is known.  The host does not know how many blocks a
+// ragged batch touches; unit v of a sequence is found by a search in the monotone bounds
 // query_start[s] / B + 2 s, which leave every sequence at least the blocks it touches.
 //
 // read_q8: code * 2^e rounded to the pool's 16-bit type (bf16 exactly), beyond its range to its
 // largest value; one thread per 16 codes of K and of V.  Both are bound by HBM.
+#include <type_traits>
+
 #include "q8.cuh"
 
 namespace pa {
@@ -40,117 +42,132 @@ __device__ __forceinline__ int find_seq(const AppendQ8Args& a, int v, int lane) 
     return lo;
 }
 
+// Finite bits of a 16-bit type's magnitude are below this, in both halves of a register.
 template <typename T>
-__global__ void __launch_bounds__(kAppendWarps * 32) append_q8_kernel(const AppendQ8Args a, int units) {
-    __shared__ float amax_of[kAppendWarps];
+constexpr uint32_t kInf2 = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+
+// Eight elements times a power of two to e4m3.
+template <typename T>
+__device__ __forceinline__ uint2 quantise8(const uint4& x, float mul) {
+    float f[8];
+    unpack8<T>(x, f);
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        w[k] = (uint32_t)f32_to_e4m3x2(f[4 * k] * mul, f[4 * k + 1] * mul) |
+               ((uint32_t)f32_to_e4m3x2(f[4 * k + 2] * mul, f[4 * k + 3] * mul) << 16);
+    return make_uint2(w[0], w[1]);
+}
+
+template <typename T, int kRows>
+__global__ void __launch_bounds__(kAppendWarps * 32) append_q8_kernel(const AppendQ8Args a, int blocks) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int B = a.block_size, Hkv = a.num_kv_heads;
-    const int wpu = B / 16;                                    // warps per unit
-    const long long u = (long long)blockIdx.x * (kAppendWarps / wpu) + warp / wpu;
-    const int part = warp % wpu;                               // 16-row part of the block
-    // unit -> (virtual block, head, K or V)
-    const int is_v = (int)(u % 2);
-    const int h = (int)(u / 2 % Hkv);
-    const long long v = u / 2 / Hkv;
-    bool live = v < units;
-    int s = 0, j = 0, L = 0;
-    NewRows nr{0, 0, false};
-    if (live) {
-        if (a.q_start) {
-            s = find_seq(a, (int)v, lane);
-            j = (int)(v - (max(0, min(a.q_start[s], a.rows)) / B + 2LL * s));
-        } else {
-            s = (int)v;
-        }
-        bool bad_len;
-        L = clamped_len(a.context_lens, s, a.max_blocks_per_seq, B, &bad_len);
-        nr = new_rows(a.q_start, a.rows, a.max_q, s, L);
-        if ((bad_len || nr.bad) && j == 0 && h == 0 && !is_v && part == 0 && lane == 0)
-            flag_status(a.status, PA_DEV_BAD_CONTEXT);
+    const unsigned u = blockIdx.x * kAppendWarps + warp;       // (virtual block, head, K or V)
+    const int is_v = u % 2, h = (int)(u / 2 % Hkv), v = (int)(u / 2 / Hkv);
+    if (v >= blocks) return;
+    int s = v, j = 0;
+    if (a.q_start) {
+        s = find_seq(a, v, lane);
+        j = (int)(v - (max(0, min(a.q_start[s], a.rows)) / B + 2LL * s));
     }
+    bool bad_len;
+    const int L = clamped_len(a.context_lens, s, a.max_blocks_per_seq, B, &bad_len);
+    const NewRows nr = new_rows(a.q_start, a.rows, a.max_q, s, L);
+    const bool speaks = h == 0 && !is_v && lane == 0;
+    if ((bad_len || nr.bad) && j == 0 && speaks) flag_status(a.status, PA_DEV_BAD_CONTEXT);
     const int p0 = L - nr.n;                                   // first new position
     const int blk_i = p0 / B + j;                              // logical block
-    live = live && j >= 0 && nr.n > 0 && blk_i <= (L - 1) / B;
-    int blk = -1, lo = 0, hi = 0;
-    if (live) {
-        blk = a.block_tables[(size_t)s * a.max_blocks_per_seq + blk_i];
-        lo = max(0, p0 - blk_i * B);                           // new rows of the block: [lo, hi)
-        hi = min(B, L - blk_i * B);
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (h == 0 && !is_v && part == 0 && lane == 0) flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
-            live = false;
-        }
-    }
-    // this warp's rows: part * 16 + 2 i + lane / 16, eight elements (lane % 16) of each
-    const int r0 = part * 16 + lane / 16, c = lane % 16;
-    uint4 x[8];
-    float amax = 0.f;
-    const T* src = nullptr;
-    if (live) {
-        const long long stride = is_v ? a.v_stride : a.k_stride;
-        src = static_cast<const T*>(is_v ? a.v : a.k) + (nr.row0 + (long long)(blk_i * B - p0)) * stride + h * kHeadDim +
-              c * 8;
+    if (j < 0 || nr.n == 0 || blk_i > (L - 1) / B) return;
+    const int blk = __ldg(a.block_tables + (size_t)s * a.max_blocks_per_seq + blk_i);
+    const int lo = max(0, p0 - blk_i * B), hi = min(B, L - blk_i * B);   // new rows of the block: [lo, hi)
+    // a batch of rows from b on: this lane has rows b + lane / 16 + 2 i, eight elements (c) of each
+    const int c = lane % 16;
+    const long long stride = is_v ? a.v_stride : a.k_stride;
+    const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (nr.row0 + (long long)(blk_i * B - p0)) * stride +
+                   h * kHeadDim + c * 8;
+    uint4 x[kRows / 2];
+    auto load = [&](int b) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = r0 + 2 * i;
+        for (int i = 0; i < kRows / 2; ++i) {
+            const int r = b + lane / 16 + 2 * i;
             x[i] = make_uint4(0, 0, 0, 0);
-            if (r >= lo && r < hi) x[i] = __ldg(reinterpret_cast<const uint4*>(src + r * stride));
+            if (r < hi) x[i] = __ldg(reinterpret_cast<const uint4*>(src + r * stride));
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float f[8];
-            unpack8<T>(x[i], f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) amax = fmaxf(amax, finite_abs(f[k]));
-        }
+    };
+    load(lo);
+    if (blk < 0 || blk >= a.num_blocks) {
+        if (speaks) flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+        return;
     }
-    amax = warp_max(amax);
-    const size_t tile = (size_t)(live ? blk : 0) * Hkv + h;
+    const size_t tile = (size_t)blk * Hkv + h;
     int8_t* exps = is_v ? a.v_exp : a.k_exp;
-    const int e_old = live ? clamp_exp(exps[tile]) : 0;
-    if (wpu > 1) {
-        if (lane == 0) amax_of[warp] = amax;
-        __syncthreads();
-        for (int i = warp - part; i < warp - part + wpu; ++i) amax = fmaxf(amax, amax_of[i]);
-    } else {
-        __syncwarp();
+    const int e_old = clamp_exp(exps[tile]);
+    // the largest magnitude, in the type's bits (their order is the values')
+    uint32_t top = 0;
+    int b = lo;   // the batch held
+    for (;;) {
+        uint32_t t = top;
+#pragma unroll
+        for (int i = 0; i < kRows / 2; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t = __vmaxu2(t, w[k] & 0x7fff7fffu);
+        }
+        if (__any_sync(0xffffffffu, __vcmpgeu2(t, kInf2<T>) != 0)) {   // infinities and NaN do not count
+#pragma unroll
+            for (int i = 0; i < kRows / 2; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t m = w[k] & 0x7fff7fffu;
+                    top = __vmaxu2(top, m & ~__vcmpgeu2(m, kInf2<T>));
+                }
+            }
+        } else {
+            top = t;
+        }
+        if (b + kRows >= hi) break;
+        b += kRows;
+        load(b);
     }
-    if (!live) return;
-    const int need = exponent_for(amax);
+    uint32_t amax = max(top & 0xffffu, top >> 16);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const int need = exponent_for(Elem<T>::to_float((uint16_t)amax));   // (every lane has read the old exponent)
     const int e = lo == 0 ? need : max(e_old, need);
     uint8_t* dst = (is_v ? a.v_cache : a.k_cache) + tile * B * kHeadDim + c * 8;
     const float mul = exp2_int(-e);
+    for (;;) {   // the batch held, then the earlier ones read again (from L2)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = r0 + 2 * i;
-        if (r >= lo && r < hi) {
-            float f[8];
-            unpack8<T>(x[i], f);
-            uint32_t w[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                w[k] = (uint32_t)f32_to_e4m3x2(f[4 * k] * mul, f[4 * k + 1] * mul) |
-                       ((uint32_t)f32_to_e4m3x2(f[4 * k + 2] * mul, f[4 * k + 3] * mul) << 16);
-            *reinterpret_cast<uint2*>(dst + r * kHeadDim) = make_uint2(w[0], w[1]);
-        } else if (r < lo && e > e_old) {
-            // an earlier row: the same values under the grown exponent
+        for (int i = 0; i < kRows / 2; ++i) {
+            const int r = b + lane / 16 + 2 * i;
+            if (r < hi) *reinterpret_cast<uint2*>(dst + r * kHeadDim) = quantise8<T>(x[i], mul);
+        }
+        if (b == lo) break;
+        b -= kRows;
+        load(b);
+    }
+    if (e > e_old && lo > 0) {
+        // earlier rows: the same values under the grown exponent
+        const float down = exp2_int(e_old - e);
+        for (int r = lane / 16; r < lo; r += 2) {
             const uint2 old = *reinterpret_cast<const uint2*>(dst + r * kHeadDim);
-            const uint32_t o[2] = {old.x, old.y};
-            const float down = exp2_int(e_old - e);
-            uint32_t w[2];
+            const uint32_t w[2] = {old.x, old.y};
+            uint32_t n[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float2 p = e4m3x2_to_float2((uint16_t)(o[k] & 0xffffu));
-                const float2 q = e4m3x2_to_float2((uint16_t)(o[k] >> 16));
-                w[k] = (uint32_t)f32_to_e4m3x2(p.x * down, p.y * down) |
+                const float2 p = e4m3x2_to_float2((uint16_t)(w[k] & 0xffffu));
+                const float2 q = e4m3x2_to_float2((uint16_t)(w[k] >> 16));
+                n[k] = (uint32_t)f32_to_e4m3x2(p.x * down, p.y * down) |
                        ((uint32_t)f32_to_e4m3x2(q.x * down, q.y * down) << 16);
             }
-            *reinterpret_cast<uint2*>(dst + r * kHeadDim) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2*>(dst + r * kHeadDim) = make_uint2(n[0], n[1]);
         }
     }
-    if (part == 0 && lane == 0) exps[tile] = (int8_t)e;
+    if (lane == 0) exps[tile] = (int8_t)e;
 }
 
 // Two fp32 to two 16-bit values, to nearest; beyond the type's range to its largest value, NaN stays.
@@ -204,13 +221,17 @@ __global__ void __launch_bounds__(256) read_q8_kernel(const ReadQ8Args a) {
 
 }  // namespace
 
+template <typename T>
+static cudaError_t launch_append(const AppendQ8Args& a, cudaStream_t stream) {
+    const int blocks = a.q_start ? a.rows / a.block_size + 2 * a.num_seqs : a.num_seqs;
+    const long long units = 2LL * blocks * a.num_kv_heads;
+    const dim3 grid((unsigned)((units + kAppendWarps - 1) / kAppendWarps)), block(kAppendWarps * 32);
+    return a.block_size == 32 ? launch_pdl(append_q8_kernel<T, 32>, grid, block, 0, stream, a, blocks)
+                              : launch_pdl(append_q8_kernel<T, 16>, grid, block, 0, stream, a, blocks);
+}
+
 cudaError_t launch_append_q8(const AppendQ8Args& a, int dtype, cudaStream_t stream) {
-    const int units = a.q_start ? a.rows / a.block_size + 2 * a.num_seqs : a.num_seqs;
-    const long long all = 2LL * units * a.num_kv_heads;
-    const int per_cta = kAppendWarps / (a.block_size / 16);
-    const dim3 grid((unsigned)((all + per_cta - 1) / per_cta)), block(kAppendWarps * 32);
-    return dtype == PA_BF16 ? launch_pdl(append_q8_kernel<__nv_bfloat16>, grid, block, 0, stream, a, units)
-                            : launch_pdl(append_q8_kernel<__half>, grid, block, 0, stream, a, units);
+    return dtype == PA_BF16 ? launch_append<__nv_bfloat16>(a, stream) : launch_append<__half>(a, stream);
 }
 
 cudaError_t launch_read_q8(const ReadQ8Args& a, int dtype, cudaStream_t stream) {

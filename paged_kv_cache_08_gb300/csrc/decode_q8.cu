@@ -42,7 +42,8 @@ constexpr int kQ8Threads = kQ8Warps * 32;
 constexpr int kTile = 16;                       // tokens per tile
 constexpr uint32_t kTileHalf = kTile * kHeadDim;   // 2 KB of K, 2 KB of V
 constexpr uint32_t kTileBytes = 2 * kTileHalf;
-constexpr int kStartUnits = 1;                  // share of a segment's start and end, in tiles
+// What a segment's start and end cost, in tiles: with more than 16 rows Q is fetched as it begins, not ahead.
+__host__ __device__ constexpr int start_units(int rows) { return rows > 16 ? 3 : 2; }
 constexpr int kQ8MaxSeqs = 1024;                // sequences of one launch (their lengths stay on chip)
 constexpr float kBaseSlack = 8.f;               // log2: P stays below 2^8
 
@@ -52,9 +53,11 @@ __host__ __device__ constexpr int piece_floats(int rows) { return rows * kHeadDi
 // Partial results of one CTA for the joining launch.
 struct CtaPieces {
     int first;      // slot 0: 0 none, 1 ends here, 2 the whole CTA is inside one segment, 3 no work
-    int last;       // slot 1 holds the head of a segment that goes on in the next CTA
-    int seq;        // of the head
-    int head;
+    int last;       // slot 1 holds the head of a segment that goes on in later CTAs
+    int end;        // the CTA in which it ends
+    int row0, rows; // its query rows
+    int head;       // its kv head
+    int pad[2];
 };
 
 struct Q8Launch {
@@ -75,22 +78,25 @@ struct Q8Smem {
     static constexpr uint32_t kOffFirst = kQ8Warps * kRing;
     static constexpr uint32_t kOffLastMl = kOffFirst + (kFirstInSmem ? kQ8Warps * piece_floats(kRows) * 4 : 0);
     static constexpr uint32_t kOffQ = kOffLastMl + kQ8Warps * kRows * 8;
-    static constexpr uint32_t kOffP = kOffQ + (kQInSmem ? kQ8Warps * NT * 16 * 32 * 4 : 0);
-    static constexpr uint32_t kOffLen = kOffP + (kQ8MaxSeqs + 1) * 8;
-    static constexpr uint32_t kOffBar = (kOffLen + kQ8MaxSeqs * 4 + 15) / 16 * 16;
-    static constexpr uint32_t kOffDesc = kOffBar + kQ8Warps * kStages * 8;
-    static constexpr uint32_t kBytes = kOffDesc + kQ8Warps * 32 + 64;
+    static constexpr uint32_t kOffCol = kOffQ + (kQInSmem ? kQ8Warps * NT * 16 * 32 * 4 : 0);
+    static constexpr uint32_t kOffDesc = kOffCol + (kQInSmem ? kQ8Warps * kRows * 8 : 0);
+    static constexpr uint32_t kOffBar = kOffDesc + kQ8Warps * 16;
+    static constexpr uint32_t kOffP = kOffBar + kQ8Warps * kStages * 8;
+    static constexpr uint32_t kOffLen = kOffP + (kQ8MaxSeqs + 4) * 4;
+    static constexpr uint32_t kOffRow0 = kOffLen + kQ8MaxSeqs * 4;   // several tokens: first row and count
+    static constexpr uint32_t kOffN = kOffRow0 + kQ8MaxSeqs * 4;
+    static constexpr uint32_t kBytes = kOffN + kQ8MaxSeqs;
     static_assert(kRing >= kRows * kHeadDim * 4, "a warp's last piece is kept in its ring");
-    static_assert(1024 + kBytes <= 227 * 1024, "shared memory of one CTA");
+    static_assert(1024 + kBytes + 64 <= 227 * 1024, "shared memory of one CTA");
 };
 
-// What a warp leaves for the end of its CTA.
+// What a warp leaves for the end of its CTA (flags, then segments as s << 16 | h).
+constexpr int kHasFirst = 1;    // a piece of a segment begun before the warp's share, ended in it
+constexpr int kHasLast = 2;     // a piece of a segment that goes on
+constexpr int kThrough = 4;     // ... and that also began before the share
+constexpr int kNoUnits = 8;
 struct WarpPieces {
-    int first;       // slot: a piece of a segment begun before the warp's share, ended in it
-    int last;        // slot: a piece of a segment that goes on; 2: it also began before
-    int empty;       // no units
-    int first_seq, first_head, last_seq, last_head;
-    int pad;
+    int flags, first_seg, last_seg, pad;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -99,12 +105,19 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr));
-    return v;
+// Products and transposes without side effects, which the compiler may move freely among loads and
+// conversions (two warps a scheduler: each has to overlap its own latencies).
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t lo_f16x2(uint32_t w) { return e4m3x2_to_f16x2((uint16_t)(w & 0xffffu)); }
@@ -132,88 +145,30 @@ __device__ __forceinline__ void store_row4(void* out, size_t at, float l, const 
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = w;
 }
 
-// Rows (query token, group member) of a segment.
-struct Seg {
-    int s, h, L;
-    int row0, n;     // first query row, new tokens
-    int p0;          // position of the first
-};
-
-template <bool kMulti>
-__device__ __forceinline__ Seg segment(const DecodeQ8Args& a, int s, int h, int L) {
-    Seg g{s, h, L, s, 1, L - 1};
-    if (kMulti) {
-        const NewRows nr = new_rows(a.q_start, a.q_rows, a.max_q, s, L);
-        g.row0 = nr.row0;
-        g.n = nr.n;
-        g.p0 = L - nr.n;
-    }
-    return g;
+// Element of query row r (token r / group, group member r % group) of kv head h's segment.
+__device__ __forceinline__ size_t row_at(const DecodeQ8Args& a, int row0, int h, int group, int r) {
+    return ((size_t)(row0 + r / group) * a.num_q_heads + (size_t)h * group + r % group) * kHeadDim;
 }
 
-__device__ __forceinline__ size_t row_offset(const DecodeQ8Args& a, const Seg& g, int group, int r) {
-    return ((size_t)(g.row0 + r / group) * a.num_q_heads + (size_t)g.h * group + r % group) * kHeadDim;
-}
-
-// One unit of the line as the lane that owns it sees it.
-struct Unit {
-    int y;           // pool row of the tile's first token; -1 no tile, -2 block outside the pool
-    int t0;          // its position
-    int seg;         // s << 16 | h
-    int flags;       // 1 the segment's first unit, 2 its last
-    int ke, ve;
-};
-
-__device__ __forceinline__ Unit unit_at(const DecodeQ8Args& a, const long long* P, const int* lens, long long u,
-                                        long long end) {
-    Unit x{-1, 0, 0, 0, 0, 0};
-    if (u >= end) return x;
-    const int Hkv = a.num_kv_heads;
-    int lo = 0, hi = a.num_seqs;                  // the last s with Hkv * P[s] <= u
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (P[mid] * Hkv <= u) lo = mid;
-        else hi = mid;
-    }
-    const long long w = P[lo + 1] - P[lo], rem = u - P[lo] * Hkv;
-    int h, r;
-    if (rem <= 0x7fffffffLL) {
-        h = (int)((uint32_t)rem / (uint32_t)w);
-        r = (int)((uint32_t)rem - (uint32_t)h * (uint32_t)w);
-    } else {
-        h = (int)(rem / w);
-        r = (int)(rem - h * w);
-    }
-    x.seg = lo << 16 | h;
-    x.flags = (r == 0 ? 1 : 0) | (r == w - 1 ? 2 : 0);
-    if (r < kStartUnits) return x;
-    x.t0 = (r - kStartUnits) * kTile;
-    const int B = a.block_size;
-    const int id = __ldg(a.block_tables + (size_t)lo * a.max_blocks_per_seq + x.t0 / B);
-    if (id < 0 || id >= a.num_blocks) {
-        flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
-        x.y = -2;
-        return x;
-    }
-    const int tile = id * Hkv + h;                // fits: num_blocks * Hkv * B < 2^31
-    x.y = tile * B + x.t0 % B;
-    x.ke = a.k_exp[tile];
-    x.ve = a.v_exp[tile];
-    return x;
-}
+// In a piece in shared memory, 16-byte chunk c of row r lies at c ^ (r / 2 % 4): the lanes that store
+// a fragment (four row pairs at once) then meet no bank conflict.
+__device__ __forceinline__ int chunk_of(int r, int c) { return r * (kHeadDim / 4) + (c ^ (r >> 1 & 3)); }
 
 template <typename T, int NT, bool kMulti>
 __global__ void __launch_bounds__(kQ8Threads, 1)
     q8_attend_kernel(const Q8Launch p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using M = Q8Smem<NT>;
-    constexpr int kStages = M::kStages;
+    constexpr int kStages = M::kStages, kStartUnits = start_units(NT * 8);
+    constexpr uint32_t kAll = 0xffffffffu;
     const DecodeQ8Args& a = p.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane / 4, t = lane % 4;
-    long long* P = reinterpret_cast<long long*>(smem + M::kOffP);
+    int* P = reinterpret_cast<int*>(smem + M::kOffP);
     int* lens = reinterpret_cast<int*>(smem + M::kOffLen);
+    int* row0_of = reinterpret_cast<int*>(smem + M::kOffRow0);
+    uint8_t* n_of = smem + M::kOffN;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::kOffBar) + warp * kStages;
     WarpPieces* wp = reinterpret_cast<WarpPieces*>(smem + M::kOffDesc);
     const uint32_t ring = smem_u32(smem) + warp * M::kRing;
@@ -222,23 +177,21 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         mbar_init(&bars[lane], 1);
         fence_mbar_init();
     }
-    if (lane == 0) {
+    if (tid == 0) {
         prefetch_map(&kmap);
         prefetch_map(&vmap);
     }
     grid_dependency_wait();
     grid_launch_dependents();
 
-    // ---- lengths and the line's prefix sums ----
-    const int S = a.num_seqs, group = a.num_q_heads / a.num_kv_heads;
+    // ---- lengths, and the units of one kv head before each sequence (P) ----
+    const int S = a.num_seqs, Hkv = a.num_kv_heads, group = a.num_q_heads / Hkv;
     {
-        constexpr int kPer = kQ8MaxSeqs / kQ8Threads;
-        __shared__ long long warp_sum_of[kQ8Warps];
-        long long mine[kPer], sum = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int s = tid * kPer + i;
-            long long w = 0;
+        __shared__ int warp_sum_of[kQ8Warps];
+        int carry = 0;
+        for (int s0 = 0; s0 < S; s0 += kQ8Threads) {
+            const int s = s0 + tid;
+            int w = 0;
             if (s < S) {
                 bool bad;
                 const int L = clamped_len(a.context_lens, s, a.max_blocks_per_seq, a.block_size, &bad);
@@ -247,41 +200,42 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     const NewRows nr = new_rows(a.q_start, a.q_rows, a.max_q, s, L);
                     n = nr.n;
                     bad |= nr.bad;
+                    row0_of[s] = nr.row0;
+                    n_of[s] = (uint8_t)n;
                 }
                 if (bad && blockIdx.x == 0) flag_status(a.status, PA_DEV_BAD_CONTEXT);
                 lens[s] = L;
                 if (L > 0 && n > 0) w = (L + kTile - 1) / kTile + kStartUnits;
             }
-            mine[i] = sum;
-            sum += w;
-        }
-        long long incl = sum;
+            int incl = w;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) warp_sum_of[warp] = incl;
-        __syncthreads();
-        long long before = incl - sum;
-        for (int i = 0; i < warp; ++i) before += warp_sum_of[i];
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(kAll, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (s0 > 0) __syncthreads();   // warp_sum_of of the round before has been read
+            if (lane == 31) warp_sum_of[warp] = incl;
+            __syncthreads();
+            int before = carry + incl - w;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (tid * kPer + i <= S) P[tid * kPer + i] = before + mine[i];
-        if (tid == kQ8Threads - 1 && S == kQ8MaxSeqs) P[S] = before + sum;
+            for (int i = 0; i < kQ8Warps; ++i) {
+                const int x = warp_sum_of[i];
+                if (i < warp) before += x;
+                carry += x;
+            }
+            if (s < S) P[s] = before;
+        }
+        if (tid == 0) P[S] = carry;
         __syncthreads();
-    }
-    if (!kMulti) {   // rows of empty sequences
-        for (int s = blockIdx.x; s < S; s += gridDim.x)
-            if (lens[s] == 0)
-                for (int i = tid; i < a.num_q_heads * kHeadDim / 8; i += kQ8Threads)
-                    reinterpret_cast<uint4*>(a.out)[(size_t)s * a.num_q_heads * kHeadDim / 8 + i] = make_uint4(0, 0, 0, 0);
     }
 
-    const long long total = P[S] * a.num_kv_heads;
-    const long long shares = (long long)gridDim.x * kQ8Warps, me = (long long)blockIdx.x * kQ8Warps + warp;
-    const long long u0 = total / shares * me + total % shares * me / shares;
-    const long long u1 = total / shares * (me + 1) + total % shares * (me + 1) / shares;
+    const long long total = (long long)P[S] * Hkv;
+    // share i of the line begins at unit floor(total * i / shares) (32-bit divisions: 64-bit ones take 0.3 us each)
+    const unsigned shares = gridDim.x * kQ8Warps, me = blockIdx.x * kQ8Warps + warp;
+    const long long each = total >> 32 ? total / shares : (long long)((unsigned)total / shares);
+    const unsigned odd = (unsigned)(total - each * shares);
+    auto share_at = [&](unsigned i) { return each * i + (odd * i) / shares; };
+    const long long u0 = share_at(me), u1 = share_at(me + 1);
     const int units = (int)(u1 - u0);
 
     // ---- per-lane fragment addresses inside a tile (128-byte swizzle: 16-byte unit ^ (row & 7)) ----
@@ -291,47 +245,65 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     const uint32_t v_off1 = kTileHalf + (2 * t + 1) * 128 + ((uint32_t)(g ^ (2 * t + 1)) << 4);
 
     float o[NT][8][4];
-    float base[NT][2], sum[NT][2], qf[NT][2];
-    int lim[NT][2];
+    float base[NT][2], sum[NT][2];
+    // of this lane's score columns (rows 2 t and 2 t + 1 of each 8): the factor to log2 units and the last
+    // position the row sees; with Q in shared memory these are kept there too
+    float qf_reg[M::kQInSmem ? 1 : NT][2];
+    int lim_reg[M::kQInSmem ? 1 : NT][2];
+    float2* qf_sm = reinterpret_cast<float2*>(smem + M::kOffCol) + warp * M::kRows;          // [NT][4] factors,
+    int2* lim_sm = reinterpret_cast<int2*>(qf_sm + M::kRows / 2);                            // [NT][4] limits
+    auto qf_of = [&](int nt) {
+        return M::kQInSmem ? qf_sm[nt * 4 + t] : make_float2(qf_reg[M::kQInSmem ? 0 : nt][0], qf_reg[M::kQInSmem ? 0 : nt][1]);
+    };
+    auto lim_of = [&](int nt) {
+        return M::kQInSmem ? lim_sm[nt * 4 + t] : make_int2(lim_reg[M::kQInSmem ? 0 : nt][0], lim_reg[M::kQInSmem ? 0 : nt][1]);
+    };
     uint32_t qreg[M::kQInSmem ? 1 : NT][16];
-    uint32_t* qsm = reinterpret_cast<uint32_t*>(smem + M::kOffQ) + warp * NT * 16 * 32 + lane;
-    Seg seg{0, 0, 0, 0, 0, 0};
-    int nrows = 0;
-    bool open_start = false, have = false;
+    uint4* qsm = reinterpret_cast<uint4*>(smem + M::kOffQ) + warp * NT * 4 * 32 + lane;
+    uint4 qn[M::kQInSmem ? 1 : NT][4];   // Q rows of the segment that comes next, as they lie in memory
+    int s = 0, h = 0, L = 0, row0 = 0, nrows = 0, p0 = 0;
     uint32_t phases = 0;
-    bool dead = false;
-    WarpPieces mine{0, 0, units == 0 ? 1 : 0, 0, 0, 0, 0, 0};
 
-    auto clear_state = [&]() {
+    // Loads of Q row 8 nt + g, dims 32 t .. 32 t + 31 of segment (s, h).
+    auto load_q = [&](int s, int h, int nt, uint4 (&to)[4]) {
+        const int first = kMulti ? row0_of[s] : s, rows = (kMulti ? n_of[s] : 1) * group, r = nt * 8 + g;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                          row_at(a, first, h, group, r < rows ? r : 0) + 32 * t);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int i = 0; i < 4; ++i) to[i] = r < rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+    };
+    // Ahead of a segment's begin, as far as registers hold the rows.
+    auto fetch_q = [&](int s, int h) {
+        if (!M::kQInSmem) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
-            base[nt][0] = base[nt][1] = -INFINITY;
-            sum[nt][0] = sum[nt][1] = 0.f;
+            for (int nt = 0; nt < NT; ++nt) load_q(s, h, nt, qn[M::kQInSmem ? 0 : nt]);
         }
     };
 
-    // Q fragments of the segment, their scales, and the positions the rows see.
-    auto begin_segment = [&](int s, int h) {
-        seg = segment<kMulti>(a, s, h, lens[s]);
-        nrows = seg.n * group;
+    // Q fragments of the segment, their scales, and the positions its rows see.
+    auto begin_segment = [&]() {
+        L = lens[s];
+        row0 = kMulti ? row0_of[s] : s;
+        const int n = kMulti ? n_of[s] : 1;
+        nrows = n * group;
+        p0 = L - n;
+        uint4 now[M::kQInSmem ? NT : 1][4];
+        if (M::kQInSmem) {   // the accumulators are not live here: room for all rows at once
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) load_q(s, h, nt, now[M::kQInSmem ? nt : 0]);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = nt * 8 + g;
-            uint4 w[4];
+            uint32_t x[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
-            if (r < nrows) {
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                                  row_offset(a, seg, group, r) + 32 * t);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = __ldg(src + i);
+            for (int i = 0; i < 4; ++i) {
+                const uint4 w = M::kQInSmem ? now[M::kQInSmem ? nt : 0][i] : qn[M::kQInSmem ? 0 : nt][i];
+                x[4 * i] = w.x;
+                x[4 * i + 1] = w.y;
+                x[4 * i + 2] = w.z;
+                x[4 * i + 3] = w.w;
             }
-            uint32_t* x = reinterpret_cast<uint32_t*>(w);
-            float scale = 1.f;
+            float2 qf = make_float2(a.scale_log2, a.scale_log2);
             if (std::is_same<T, __nv_bfloat16>::value) {
                 float amax = 0.f;
 #pragma unroll
@@ -339,34 +311,224 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     const float2 f = Elem<T>::to_float2(x[i]);
                     amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
                 }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 2));
                 // largest element into [2^14, 2^15)
                 const int up = max(-126, min(126, 14 - ((__float_as_int(amax) >> 23) - 127)));
-                const float mul = exp2_int(up);
-                scale = exp2_int(-up);
+                const float mul = exp2_int(up), scale = exp2_int(-up);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float2 f = Elem<T>::to_float2(x[i]);
                     x[i] = Elem<__half>::pack2(f.x * mul, f.y * mul);
                 }
+                qf.x = __shfl_sync(kAll, scale, (2 * t) * 4) * a.scale_log2;
+                qf.y = __shfl_sync(kAll, scale, (2 * t + 1) * 4) * a.scale_log2;
             }
+            if (M::kQInSmem) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (M::kQInSmem) qsm[(nt * 16 + i) * 32] = x[i];
-                else qreg[M::kQInSmem ? 0 : nt][i] = x[i];
+                for (int i = 0; i < 4; ++i)
+                    qsm[(nt * 4 + i) * 32] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) qreg[M::kQInSmem ? 0 : nt][i] = x[i];
             }
-            // this lane's score columns are rows 2 t and 2 t + 1
-            qf[nt][0] = __shfl_sync(0xffffffffu, scale, (2 * t) * 4) * a.scale_log2;
-            qf[nt][1] = __shfl_sync(0xffffffffu, scale, (2 * t + 1) * 4) * a.scale_log2;
+            int lim[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int col = nt * 8 + 2 * t + c;
-                lim[nt][c] = kMulti && col < nrows ? seg.p0 + col / group : seg.L - 1;
+                lim[c] = kMulti && col < nrows ? p0 + col / group : L - 1;
+                base[nt][c] = -INFINITY;
+                sum[nt][c] = 0.f;
+            }
+            if (M::kQInSmem) {
+                if (g == 0) {
+                    qf_sm[nt * 4 + t] = qf;
+                    lim_sm[nt * 4 + t] = make_int2(lim[0], lim[1]);
+                }
+            } else {
+                qf_reg[M::kQInSmem ? 0 : nt][0] = qf.x;
+                qf_reg[M::kQInSmem ? 0 : nt][1] = qf.y;
+                lim_reg[M::kQInSmem ? 0 : nt][0] = lim[0];
+                lim_reg[M::kQInSmem ? 0 : nt][1] = lim[1];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
+        }
+        if (M::kQInSmem) __syncwarp();
+    };
+
+    // One tile of tokens t0 .. t0 + 15 against the first K x 8 rows.
+    auto run_tile = [&](auto kc, uint32_t tile_at, int t0, int ke, int ve) {
+        constexpr int K = decltype(kc)::value;
+        const uint8_t* tile = smem + tile_at;
+        const uint4 k0 = *reinterpret_cast<const uint4*>(tile + k_off0), k1 = *reinterpret_cast<const uint4*>(tile + k_off1);
+        const uint4 k2 = *reinterpret_cast<const uint4*>(tile + k_off0 + 1024);
+        const uint4 k3 = *reinterpret_cast<const uint4*>(tile + k_off1 + 1024);
+        uint4 v0 = *reinterpret_cast<const uint4*>(tile + v_off0), v1 = *reinterpret_cast<const uint4*>(tile + v_off1);
+        uint4 v2 = *reinterpret_cast<const uint4*>(tile + v_off0 + 1024);
+        uint4 v3 = *reinterpret_cast<const uint4*>(tile + v_off1 + 1024);
+        // S = K Q^T
+        float sc[K][4];
+        {
+            const uint32_t ka[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+            const uint32_t kb[8] = {k2.x, k2.y, k2.z, k2.w, k3.x, k3.y, k3.z, k3.w};
+            float odd[K == 1 ? 1 : K][4];   // one tile of rows: odd steps on their own, for two short chains
+#pragma unroll
+            for (int nt = 0; nt < K; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sc[nt][c] = odd[nt][c] = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint4 b[K];
+#pragma unroll
+                for (int nt = 0; nt < K; ++nt) {
+                    if (M::kQInSmem) b[nt] = qsm[(nt * 4 + q) * 32];
+                    else
+                        b[nt] = make_uint4(qreg[M::kQInSmem ? 0 : nt][4 * q], qreg[M::kQInSmem ? 0 : nt][4 * q + 1],
+                                           qreg[M::kQInSmem ? 0 : nt][4 * q + 2], qreg[M::kQInSmem ? 0 : nt][4 * q + 3]);
+                }
+                {
+                    const uint32_t a0 = lo_f16x2(ka[2 * q]), a1 = lo_f16x2(kb[2 * q]), a2 = hi_f16x2(ka[2 * q]),
+                                   a3 = hi_f16x2(kb[2 * q]);
+#pragma unroll
+                    for (int nt = 0; nt < K; ++nt) mma_f16(sc[nt], a0, a1, a2, a3, b[nt].x, b[nt].y);
+                }
+                {
+                    const uint32_t a0 = lo_f16x2(ka[2 * q + 1]), a1 = lo_f16x2(kb[2 * q + 1]),
+                                   a2 = hi_f16x2(ka[2 * q + 1]), a3 = hi_f16x2(kb[2 * q + 1]);
+#pragma unroll
+                    for (int nt = 0; nt < K; ++nt) mma_f16(K == 1 ? odd[nt] : sc[nt], a0, a1, a2, a3, b[nt].z, b[nt].w);
+                }
+            }
+            if (K == 1) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sc[0][c] += odd[0][c];
             }
         }
-        clear_state();
-        have = true;
+
+        // x = score in log2 units + ve - base; positions a row does not see to -inf
+        const float ks = exp2_int(ke), vef = (float)ve, unscale = exp2_int(-ve);
+        const bool masked = t0 + kTile > p0 + 1;
+        bool nan_v = false;
+        float x[K][4];
+        auto scores = [&]() {
+#pragma unroll
+            for (int nt = 0; nt < K; ++nt) {
+                const float2 qf = qf_of(nt);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(sc[nt][c], (c & 1 ? qf.y : qf.x) * ks, vef - base[nt][c & 1]);
+            }
+            if (masked) {
+#pragma unroll
+                for (int nt = 0; nt < K; ++nt) {
+                    const int2 lim = lim_of(nt);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (t0 + g + (c >> 1) * 8 > (c & 1 ? lim.y : lim.x)) x[nt][c] = -INFINITY;
+                }
+            }
+        };
+        scores();
+        if (masked) {
+            // rows behind the last token hold anything: zero codes
+            const int left = L - t0;
+            if (2 * t >= left) v0 = make_uint4(0, 0, 0, 0);
+            if (2 * t + 1 >= left) v1 = make_uint4(0, 0, 0, 0);
+            if (2 * t + 8 >= left) v2 = make_uint4(0, 0, 0, 0);
+            if (2 * t + 9 >= left) v3 = make_uint4(0, 0, 0, 0);
+            if (kMulti) {
+                // a NaN of a token that some rows do not see must not reach them through 0 * NaN
+                auto nans = [](uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); };
+                auto any4 = [&](const uint4& v) { return nans(v.x) | nans(v.y) | nans(v.z) | nans(v.w); };
+                nan_v = __any_sync(kAll, (any4(v0) | any4(v1) | any4(v2) | any4(v3)) != 0);
+                if (nan_v) {
+                    auto drop = [&](uint4& v) {
+                        v.x &= ~nans(v.x);
+                        v.y &= ~nans(v.y);
+                        v.z &= ~nans(v.z);
+                        v.w &= ~nans(v.w);
+                    };
+                    drop(v0);
+                    drop(v1);
+                    drop(v2);
+                    drop(v3);
+                }
+            }
+        }
+        float top = x[0][0];   // NaN does not move a base
+#pragma unroll
+        for (int nt = 0; nt < K; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) top = fmaxf(top, x[nt][c]);
+        // a column without a base yet (-inf) has +inf here as soon as it sees a token
+        if (__any_sync(kAll, top > kBaseSlack)) {
+#pragma unroll
+            for (int nt = 0; nt < K; ++nt) {
+                const float2 qf = qf_of(nt);
+                const int2 lim = lim_of(nt);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float f1 = (c ? qf.y : qf.x) * ks;
+                    const int last = c ? lim.y : lim.x;
+                    float m = base[nt][c];
+                    if (!masked || t0 + g <= last) m = fmaxf(m, fmaf(sc[nt][c], f1, vef));
+                    if (!masked || t0 + g + 8 <= last) m = fmaxf(m, fmaf(sc[nt][c + 2], f1, vef));
+#pragma unroll
+                    for (int k = 4; k < 32; k <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
+                    const float f = base[nt][c] == -INFINITY ? 0.f : ex2(base[nt][c] - m);
+                    base[nt][c] = m;
+                    sum[nt][c] *= f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        o[nt][k][c] *= f;
+                        o[nt][k][c + 2] *= f;
+                    }
+                }
+            }
+            scores();
+        }
+        uint32_t b0[K], b1[K];
+#pragma unroll
+        for (int nt = 0; nt < K; ++nt) {
+            float pr[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) pr[c] = ex2(x[nt][c]);
+            sum[nt][0] = fmaf(pr[0] + pr[2], unscale, sum[nt][0]);
+            sum[nt][1] = fmaf(pr[1] + pr[3], unscale, sum[nt][1]);
+            b0[nt] = transpose8x8(Elem<__half>::pack2(pr[0], pr[1]));
+            b1[nt] = transpose8x8(Elem<__half>::pack2(pr[2], pr[3]));
+        }
+        // O += V^T P^T
+        const uint32_t va[4] = {v0.x, v0.y, v0.z, v0.w}, vb[4] = {v1.x, v1.y, v1.z, v1.w};
+        const uint32_t vc[4] = {v2.x, v2.y, v2.z, v2.w}, vd[4] = {v3.x, v3.y, v3.z, v3.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t sel = e ? 0x7362 : 0x5140;   // dims 2e, 2e+1 of tokens (first, second)
+                const uint32_t ab = __byte_perm(va[q], vb[q], sel), cd = __byte_perm(vc[q], vd[q], sel);
+                const uint32_t a0 = lo_f16x2(ab), a1 = hi_f16x2(ab), a2 = lo_f16x2(cd), a3 = hi_f16x2(cd);
+#pragma unroll
+                for (int nt = 0; nt < K; ++nt) mma_f16(o[nt][2 * q + e], a0, a1, a2, a3, b0[nt], b1[nt]);
+            }
+        }
+        if (kMulti && nan_v) {
+            // rare: NaN into the dims and rows that see such a token
+            for (int j = 0; j < min(kTile, L - t0); ++j) {
+                const uint4 v = *reinterpret_cast<const uint4*>(tile + kTileHalf + j * 128 + ((g ^ (j & 7)) << 4));
+                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int d = 0; d < 16; ++d)
+                    if (((vw[d / 4] >> (8 * (d % 4))) & 0x7f) == 0x7f)
+#pragma unroll
+                        for (int nt = 0; nt < K; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                if (t0 + j <= (c ? lim_of(nt).y : lim_of(nt).x)) o[nt][d / 2][c + 2 * (d % 2)] = __int_as_float(0x7fffffff);
+            }
+        }
     };
 
     // Sum over the lanes that share a column.
@@ -376,11 +538,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                for (int m = 4; m < 32; m <<= 1) sum[nt][c] += __shfl_xor_sync(0xffffffffu, sum[nt][c], m);
+                for (int m = 4; m < 32; m <<= 1) sum[nt][c] += __shfl_xor_sync(kAll, sum[nt][c], m);
             }
     };
 
-    auto store_piece = [&](float* slot, float2* ml) {
+    auto store_piece = [&](float4* slot, float2* ml) {
         finish_sums();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -388,10 +550,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             for (int c = 0; c < 2; ++c) {
                 const int r = nt * 8 + 2 * t + c;
                 if (r < nrows) {
-                    float* dst = slot + r * kHeadDim;
 #pragma unroll
                     for (int i = 0; i < 8; i += 2)
-                        *reinterpret_cast<float4*>(dst + g * 16 + 2 * i) =
+                        slot[chunk_of(r, g * 4 + i / 2)] =
                             make_float4(o[nt][i][c], o[nt][i][c + 2], o[nt][i + 1][c], o[nt][i + 1][c + 2]);
                     if (g == 0) ml[r] = make_float2(base[nt][c], sum[nt][c]);
                 }
@@ -410,7 +571,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     uint32_t w[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) w[i] = Elem<T>::pack2(o[nt][i][c] * inv, o[nt][i][c + 2] * inv);
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row_offset(a, seg, group, r) +
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row_at(a, row0, h, group, r) +
                                                           g * 16);
                     dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                     dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -421,17 +582,57 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     // pieces of warp w: the first in memory of its own, the last in its ring (every copy has landed)
     const int slot_rows = M::kFirstInSmem ? M::kRows : p.rows;
     auto first_of = [&](int w) {
-        return M::kFirstInSmem ? reinterpret_cast<float*>(smem + M::kOffFirst) + w * piece_floats(M::kRows)
-                               : p.firsts + ((size_t)blockIdx.x * kQ8Warps + w) * piece_floats(p.rows);
+        return reinterpret_cast<float4*>(
+            M::kFirstInSmem ? reinterpret_cast<float*>(smem + M::kOffFirst) + w * piece_floats(M::kRows)
+                            : p.firsts + ((size_t)blockIdx.x * kQ8Warps + w) * piece_floats(p.rows));
     };
-    auto last_of = [&](int w) { return reinterpret_cast<float*>(smem + w * M::kRing); };
-    auto first_ml_of = [&](int w) { return reinterpret_cast<float2*>(first_of(w) + slot_rows * kHeadDim); };
+    auto last_of = [&](int w) { return reinterpret_cast<float4*>(smem + w * M::kRing); };
+    auto first_ml_of = [&](int w) { return reinterpret_cast<float2*>(first_of(w) + slot_rows * kHeadDim / 4); };
     auto last_ml_of = [&](int w) { return reinterpret_cast<float2*>(smem + M::kOffLastMl) + w * M::kRows; };
 
     // ---- the stream ----
+    WarpPieces mine{units == 0 ? kNoUnits : 0, 0, 0, 0};
     if (units > 0) {
-        __syncwarp();
-        Unit A = unit_at(a, P, lens, u0 + lane, u1), Bn{-1, 0, 0, 0, 0, 0};
+        {   // the last s with P[s] * Hkv <= u0
+            unsigned m = __ballot_sync(kAll, lane * 32 < S && (long long)P[min(lane * 32, S)] * Hkv <= u0);
+            s = (31 - __clz(m)) * 32;
+            m = __ballot_sync(kAll, s + lane < S && (long long)P[min(s + lane, S)] * Hkv <= u0);
+            s += 31 - __clz(m);
+        }
+        // of the unit this lane owns in a window of 32: the pool row of its tile's first token (-1: a start
+        // unit or none, -2: a block outside the pool) and its block's exponents
+        int A_y = -1, A_ke = 0, A_ve = 0, B_y = -1, B_ke = 0, B_ve = 0, lane_s = s;
+        auto look = [&](int i, int& y, int& ke, int& ve) {   // unit u0 + i; i grows from call to call
+            y = -1;
+            if (i >= units) return;
+            const long long u = u0 + i;
+            while ((long long)P[lane_s + 1] * Hkv <= u) ++lane_s;
+            const uint32_t w = P[lane_s + 1] - P[lane_s];
+            const unsigned long long rem = u - (long long)P[lane_s] * Hkv;
+            const int hh = rem <= 0xffffffffu ? (uint32_t)rem / w : (int)(rem / w);
+            const int r = (int)(rem - (unsigned long long)hh * w);
+            if (r < kStartUnits) return;
+            const int t0 = (r - kStartUnits) * kTile, B = a.block_size;
+            const int id = __ldg(a.block_tables + (size_t)lane_s * a.max_blocks_per_seq + t0 / B);
+            if (id < 0 || id >= a.num_blocks) {
+                flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+                y = -2;
+                return;
+            }
+            const int tile = id * Hkv + hh;                // fits: num_blocks * Hkv * B < 2^31
+            y = tile * B + t0 % B;
+            ke = __ldg(a.k_exp + tile);
+            ve = __ldg(a.v_exp + tile);
+        };
+        int r;   // unit of the segment at the head of the share
+        {
+            const uint32_t w = P[s + 1] - P[s];
+            const unsigned long long rem = u0 - (long long)P[s] * Hkv;
+            h = rem <= 0xffffffffu ? (uint32_t)rem / w : (int)(rem / w);
+            r = (int)(rem - (unsigned long long)h * w);
+        }
+        fetch_q(s, h);
+        look(lane, A_y, A_ke, A_ve);
         auto issue = [&](int j, int y) {   // by the lane that owns unit j
             const int st = j % kStages;
             const uint32_t dst = ring + st * kTileBytes;
@@ -439,325 +640,268 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             tma_load_2d(dst, &kmap, 0, y, &bars[st]);
             tma_load_2d(dst + kTileHalf, &vmap, 0, y, &bars[st]);
         };
-        if (lane < kStages && A.y >= 0) issue(lane, A.y);
-        {   // the share may begin inside a segment
-            const int sh = __shfl_sync(0xffffffffu, A.seg, 0), fl = __shfl_sync(0xffffffffu, A.flags, 0);
-            open_start = !(fl & 1);
-            if (open_start) {
-                begin_segment(sh >> 16, sh & 0xffff);
-                mine.first_seq = seg.s;
-                mine.first_head = seg.h;
-            }
-        }
+        if (lane < kStages && A_y >= 0) issue(lane, A_y);
+        bool dead = false;
         int i = 0;
-        for (; i < units; ++i) {
-            const int w = i & 31;
-            if (w == 0) {
-                if (i > 0) A = Bn;
-                if (i + 32 < units) Bn = unit_at(a, P, lens, u0 + i + 32 + lane, u1);
-            }
-            const int y = __shfl_sync(0xffffffffu, A.y, w), flags = __shfl_sync(0xffffffffu, A.flags, w);
-            if (flags & 1) {
-                const int sh = __shfl_sync(0xffffffffu, A.seg, w);
-                begin_segment(sh >> 16, sh & 0xffff);
-            }
-            if (y >= 0) {
-                const int t0 = __shfl_sync(0xffffffffu, A.t0, w);
-                const int ke = clamp_exp(__shfl_sync(0xffffffffu, A.ke, w)), ve = clamp_exp(__shfl_sync(0xffffffffu, A.ve, w));
-                const int st = i % kStages;
-                if (!mbar_wait_bounded(&bars[st], (phases >> st) & 1)) {
-                    flag_status(a.status, PA_DEV_TIMEOUT);
-                    dead = true;
+        while (i < units) {
+            // segment (s, h) from its unit r on
+            const int left = P[s + 1] - P[s] - r, stop = min(units, i + left);
+            const bool from_before = r > 0, ends = i + left <= units;
+            begin_segment();
+            const int this_s = s, this_h = h;
+            int next_s = s, next_h = h + 1;
+            if (i + left < units) {
+                if (next_h == Hkv) {
+                    next_h = 0;
+                    do ++next_s;
+                    while (P[next_s + 1] == P[next_s]);
                 }
-                dead = __any_sync(0xffffffffu, dead);
-                if (dead) break;
-                phases ^= 1u << st;
-                const uint32_t tile = ring + st * kTileBytes;
-
-                // S = K Q^T
-                float x[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
-                {
-                    const uint4 k0 = lds128(tile + k_off0), k1 = lds128(tile + k_off1);
-                    const uint4 k2 = lds128(tile + k_off0 + 1024), k3 = lds128(tile + k_off1 + 1024);
-                    const uint32_t ka[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
-                    const uint32_t kb[8] = {k2.x, k2.y, k2.z, k2.w, k3.x, k3.y, k3.z, k3.w};
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) {
-                        const uint32_t a0 = lo_f16x2(ka[s]), a1 = lo_f16x2(kb[s]), a2 = hi_f16x2(ka[s]),
-                                       a3 = hi_f16x2(kb[s]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const uint32_t b0 = M::kQInSmem ? qsm[(nt * 16 + 2 * s) * 32] : qreg[M::kQInSmem ? 0 : nt][2 * s];
-                            const uint32_t b1 =
-                                M::kQInSmem ? qsm[(nt * 16 + 2 * s + 1) * 32] : qreg[M::kQInSmem ? 0 : nt][2 * s + 1];
-                            mma16816<__half>(x[nt], a0, a1, a2, a3, b0, b1);
+                fetch_q(next_s, next_h);
+            }
+            const int tiles_of_8 = (nrows + 7) / 8;
+            for (; i < stop; ++i, ++r) {
+                const int w = i & 31;
+                if (w == 0) {
+                    if (i > 0) {
+                        A_y = B_y;
+                        A_ke = B_ke;
+                        A_ve = B_ve;
+                    }
+                    if (i + 32 < units) look(i + 32 + lane, B_y, B_ke, B_ve);
+                }
+                const int y = __shfl_sync(kAll, A_y, w);
+                if (y >= 0) {
+                    const int ke = clamp_exp(__shfl_sync(kAll, A_ke, w)), ve = clamp_exp(__shfl_sync(kAll, A_ve, w));
+                    const int st = i % kStages;
+                    if (!mbar_wait_bounded(&bars[st], (phases >> st) & 1)) {
+                        flag_status(a.status, PA_DEV_TIMEOUT);
+                        dead = true;
+                    }
+                    dead = __any_sync(kAll, dead);
+                    if (dead) break;
+                    phases ^= 1u << st;
+                    const uint32_t tile = warp * M::kRing + st * kTileBytes;
+                    const int t0 = (r - kStartUnits) * kTile;
+                    if (!kMulti || NT == 1) {
+                        run_tile(std::integral_constant<int, NT>{}, tile, t0, ke, ve);
+                    } else {
+                        switch (tiles_of_8) {
+                            case 1: run_tile(std::integral_constant<int, 1>{}, tile, t0, ke, ve); break;
+                            case 2: run_tile(std::integral_constant<int, 2>{}, tile, t0, ke, ve); break;
+                            case 3: run_tile(std::integral_constant<int, NT < 3 ? NT : 3>{}, tile, t0, ke, ve); break;
+                            default: run_tile(std::integral_constant<int, NT>{}, tile, t0, ke, ve); break;
                         }
                     }
                 }
-                uint4 v0 = lds128(tile + v_off0), v1 = lds128(tile + v_off1);
-                uint4 v2 = lds128(tile + v_off0 + 1024), v3 = lds128(tile + v_off1 + 1024);
-
-                // x = score in log2 units + ve; positions a row does not see to -inf
-                const float ks = exp2_int(ke), vef = (float)ve, unscale = exp2_int(-ve);
-                const bool masked = t0 + kTile > seg.p0 + 1;
-                bool nan_v = false;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(x[nt][c], qf[nt][c & 1] * ks, vef);
-                if (masked) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (t0 + g + (c >> 1) * 8 > lim[nt][c & 1]) x[nt][c] = -INFINITY;
-                    // rows behind the last token hold anything: zero codes
-                    const int left = seg.L - t0;
-                    if (2 * t >= left) v0 = make_uint4(0, 0, 0, 0);
-                    if (2 * t + 1 >= left) v1 = make_uint4(0, 0, 0, 0);
-                    if (2 * t + 8 >= left) v2 = make_uint4(0, 0, 0, 0);
-                    if (2 * t + 9 >= left) v3 = make_uint4(0, 0, 0, 0);
-                    if (kMulti) {
-                        // a NaN of a token that some rows do not see must not reach them through 0 * NaN
-                        auto nans = [](uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); };
-                        auto any4 = [&](const uint4& v) { return nans(v.x) | nans(v.y) | nans(v.z) | nans(v.w); };
-                        nan_v = __any_sync(0xffffffffu, (any4(v0) | any4(v1) | any4(v2) | any4(v3)) != 0);
-                        if (nan_v) {
-                            auto drop = [&](uint4& v) {
-                                v.x &= ~nans(v.x);
-                                v.y &= ~nans(v.y);
-                                v.z &= ~nans(v.z);
-                                v.w &= ~nans(v.w);
-                            };
-                            drop(v0);
-                            drop(v1);
-                            drop(v2);
-                            drop(v3);
-                        }
-                    }
-                }
-                bool move = false;   // a column without a base yet (-inf) takes one as soon as it sees a token
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        move |= fmaxf(x[nt][c], x[nt][c + 2]) > base[nt][c] + kBaseSlack;
-                if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float m = fmaxf(x[nt][c], x[nt][c + 2]);
-#pragma unroll
-                            for (int k = 4; k < 32; k <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-                            m = fmaxf(m, base[nt][c]);
-                            const float f = base[nt][c] == -INFINITY ? 0.f : ex2(base[nt][c] - m);
-                            base[nt][c] = m;
-                            sum[nt][c] *= f;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                o[nt][k][c] *= f;
-                                o[nt][k][c + 2] *= f;
-                            }
-                        }
-                }
-                uint32_t b0[NT], b1[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float pr[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        pr[c] = ex2(x[nt][c] - base[nt][c & 1]);
-                        if (masked && t0 + g + (c >> 1) * 8 > lim[nt][c & 1]) pr[c] = 0.f;
-                    }
-                    sum[nt][0] = fmaf(pr[0] + pr[2], unscale, sum[nt][0]);
-                    sum[nt][1] = fmaf(pr[1] + pr[3], unscale, sum[nt][1]);
-                    b0[nt] = movmatrix_trans(Elem<__half>::pack2(pr[0], pr[1]));
-                    b1[nt] = movmatrix_trans(Elem<__half>::pack2(pr[2], pr[3]));
-                }
-                // O += V^T P^T
-                const uint32_t va[4] = {v0.x, v0.y, v0.z, v0.w}, vb[4] = {v1.x, v1.y, v1.z, v1.w};
-                const uint32_t vc[4] = {v2.x, v2.y, v2.z, v2.w}, vd[4] = {v3.x, v3.y, v3.z, v3.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t sel = e ? 0x7362 : 0x5140;   // dims 2e, 2e+1 of tokens (first, second)
-                        const uint32_t ab = __byte_perm(va[q], vb[q], sel), cd = __byte_perm(vc[q], vd[q], sel);
-                        const uint32_t a0 = lo_f16x2(ab), a1 = hi_f16x2(ab), a2 = lo_f16x2(cd), a3 = hi_f16x2(cd);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816<__half>(o[nt][2 * q + e], a0, a1, a2, a3, b0[nt], b1[nt]);
-                    }
-                }
-                if (kMulti && nan_v) {
-                    // rare: NaN into the dims and rows that see such a token
-                    for (int j = 0; j < min(kTile, seg.L - t0); ++j) {
-                        const uint4 v = lds128(tile + kTileHalf + j * 128 + ((uint32_t)(g ^ (j & 7)) << 4));
-                        const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int d = 0; d < 16; ++d)
-                            if (((vw[d / 4] >> (8 * (d % 4))) & 0x7f) == 0x7f)
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                    for (int c = 0; c < 2; ++c)
-                                        if (t0 + j <= lim[nt][c]) o[nt][d / 2][c + 2 * (d % 2)] = __int_as_float(0x7fffffff);
-                    }
+                // every lane has the tile in registers: its stage takes the unit kStages further on
+                __syncwarp();
+                const int j = i + kStages;
+                if (j < units && lane == (j & 31)) {
+                    const int yj = (j >> 5) == (i >> 5) ? A_y : B_y;
+                    if (yj >= 0) issue(j, yj);
                 }
             }
-            // every lane has the tile in registers: its stage takes the unit kStages further on
-            __syncwarp();
-            const int j = i + kStages;
-            if (j < units && lane == (j & 31)) {
-                const int yj = (j >> 5) == (i >> 5) ? A.y : Bn.y;
-                if (yj >= 0) issue(j, yj);
+            if (dead) break;
+            if (!ends) {
+                store_piece(last_of(warp), last_ml_of(warp));
+                mine.flags |= kHasLast | (from_before ? kThrough : 0);
+                mine.last_seg = this_s << 16 | this_h;
+            } else if (from_before) {
+                store_piece(first_of(warp), first_ml_of(warp));
+                mine.flags |= kHasFirst;
+                mine.first_seg = this_s << 16 | this_h;
+            } else {
+                store_out();
             }
-            if (flags & 2) {
-                if (open_start) {
-                    store_piece(first_of(warp), first_ml_of(warp));
-                    mine.first = 1;
-                } else {
-                    store_out();
-                }
-                open_start = false;
-                have = false;
-            }
+            s = next_s;
+            h = next_h;
+            r = 0;
         }
         if (dead) {   // let the copies in flight land (again with a limit) before the CTA's memory is given up
             for (int j = i; j < min(units, i + kStages); ++j) {
-                const int yj = __shfl_sync(0xffffffffu, (j >> 5) == (i >> 5) ? A.y : Bn.y, j & 31);
+                const int yj = __shfl_sync(kAll, (j >> 5) == (i >> 5) ? A_y : B_y, j & 31);
                 if (yj >= 0) mbar_wait_bounded(&bars[j % kStages], (phases >> (j % kStages)) & 1);
             }
-            have = false;
-            __syncwarp();
-        }
-        if (have) {
-            store_piece(last_of(warp), last_ml_of(warp));
-            mine.last = open_start ? 2 : 1;
-            mine.last_seq = seg.s;
-            mine.last_head = seg.h;
         }
     }
     if (lane == 0) wp[warp] = mine;
     __syncthreads();
 
     // ---- join the pieces of cut segments ----
-    // Warps in order: a first piece ends the chain that is open (or one from before this CTA), a last
-    // piece goes on with it (2) or opens one (1).  Of a chain ws .. we, warp we gives its first piece if
-    // the chain ends there, every other warp its last.
-    CtaPieces left{3, 0, 0, 0};
-    auto join = [&](int ws, int we, bool before, bool closed, int s, int h) {
-        const Seg sg = segment<kMulti>(a, s, h, lens[s]);
-        float* to = p.parts + ((size_t)blockIdx.x * 2 + (before ? 0 : 1)) * piece_floats(p.rows);
-        for (int e = tid; e < sg.n * group * 32; e += kQ8Threads) {
-            const int r = e / 32, d = e % 32 * 4;
-            float m = -INFINITY, l = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = ws; w <= we; ++w) {
-                if (wp[w].empty) continue;
-                const bool first = closed && w == we;
-                add_piece(m, l, acc, (first ? first_ml_of(w) : last_ml_of(w))[r],
-                          *reinterpret_cast<const float4*>((first ? first_of(w) : last_of(w)) + r * kHeadDim + d));
+    // A first piece ends the chain of pieces that is open (or one from before this CTA), a last piece goes
+    // on with it (kThrough) or opens one.  Of a chain ws .. we, warp we gives its first piece if the chain
+    // ends there, every other warp its last.  The rows of all chains are dealt to the warps, four at a time.
+    int left_first = 3, left_last = 0, left_seg = 0;
+    {
+        const WarpPieces x = wp[lane % kQ8Warps];
+        const unsigned low = (1u << kQ8Warps) - 1;
+        const unsigned some = ~__ballot_sync(kAll, x.flags & kNoUnits) & low;
+        const unsigned firsts = __ballot_sync(kAll, x.flags & kHasFirst) & low;
+        const unsigned lasts = __ballot_sync(kAll, x.flags & kHasLast) & low;
+        const unsigned opens = lasts & ~__ballot_sync(kAll, x.flags & kThrough);
+        const int last_warp = some ? 31 - __clz(some) : 0;
+        // events: a first piece at its warp, and at kQ8Warps the chain still open at the end
+        unsigned events = firsts | ((lasts >> last_warp & 1) << kQ8Warps);
+        if (some) left_first = 0;
+        if (events) {
+            const int e = __ffs(events) - 1;
+            if (!(opens & ((1u << e) - 1))) left_first = e < kQ8Warps ? 1 : 2;
+        }
+        if ((events >> kQ8Warps) && (opens >> (firsts ? 31 - __clz(firsts) : 0))) {
+            left_last = 1;
+            left_seg = __shfl_sync(kAll, x.last_seg, last_warp);
+        }
+        const int batches = (p.rows + 3) / 4, items = __popc(events) * batches;
+        for (int item = warp; item < items; item += kQ8Warps) {
+            unsigned ev = events;
+            int k = item;
+            for (; k >= batches; k -= batches) ev &= ev - 1;
+            const int we = __ffs(ev) - 1;
+            const unsigned below = events & ((1u << we) - 1);
+            const bool closed = we < kQ8Warps;
+            const unsigned opener = opens & ((1u << we) - 1) & ~((1u << (below ? 31 - __clz(below) : 0)) - 1);
+            const bool before = opener == 0;
+            const int ws = before ? 0 : __ffs(opener) - 1;
+            const unsigned pieces = some & ~((1u << ws) - 1) & ((2u << we) - 1);
+            const int seg = __shfl_sync(kAll, closed ? x.first_seg : x.last_seg, closed ? we : last_warp);
+            const int sg = seg >> 16, hh = seg & 0xffff, r0 = k * 4;
+            const int first = kMulti ? row0_of[sg] : sg, rows = (kMulti ? n_of[sg] : 1) * group;
+            if (r0 >= rows) continue;
+            float* to = p.parts + ((size_t)blockIdx.x * 2 + (before ? 0 : 1)) * piece_floats(p.rows);
+            // four rows at a time: lane 8 i + w weighs warp w's piece of row i, then every lane has four
+            // elements of each row
+            const int w = lane % kQ8Warps, rw = r0 + lane / kQ8Warps;
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if ((pieces >> w & 1) && rw < rows) ml = (closed && w == we ? first_ml_of(w) : last_ml_of(w))[rw];
+            float m = ml.x;
+#pragma unroll
+            for (int k = 1; k < kQ8Warps; k <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
+            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+            float l = f * ml.y;
+#pragma unroll
+            for (int k = 1; k < kQ8Warps; k <<= 1) l += __shfl_xor_sync(kAll, l, k);
+            float4 acc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (unsigned todo = pieces; todo; todo &= todo - 1) {
+                const int pw = __ffs(todo) - 1;
+                const float4* slot = closed && pw == we ? first_of(pw) : last_of(pw);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float fw = __shfl_sync(kAll, f, i * kQ8Warps + pw);
+                    if (r0 + i < rows) {
+                        const float4 v = slot[chunk_of(r0 + i, lane)];
+                        acc[i].x = fmaf(fw, v.x, acc[i].x);
+                        acc[i].y = fmaf(fw, v.y, acc[i].y);
+                        acc[i].z = fmaf(fw, v.z, acc[i].z);
+                        acc[i].w = fmaf(fw, v.w, acc[i].w);
+                    }
+                }
             }
-            if (closed && !before) {
-                store_row4<T>(a.out, row_offset(a, sg, group, r) + d, l, acc);
-            } else {
-                *reinterpret_cast<float4*>(to + r * kHeadDim + d) = acc;
-                if (d == 0) reinterpret_cast<float2*>(to + p.rows * kHeadDim)[r] = make_float2(m, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float mi = __shfl_sync(kAll, m, i * kQ8Warps), li = __shfl_sync(kAll, l, i * kQ8Warps);
+                const int r = r0 + i;
+                if (r < rows) {
+                    if (closed && !before) {
+                        store_row4<T>(a.out, row_at(a, first, hh, group, r) + lane * 4, li, acc[i]);
+                    } else {
+                        *reinterpret_cast<float4*>(to + r * kHeadDim + lane * 4) = acc[i];
+                        if (lane == 0) reinterpret_cast<float2*>(to + p.rows * kHeadDim)[r] = make_float2(mi, li);
+                    }
+                }
             }
-        }
-        if (before) {
-            left.first = closed ? 1 : 2;
-        } else if (!closed) {
-            left.last = 1;
-            left.seq = s;
-            left.head = h;
-        }
-    };
-    int ws = -1;
-    bool before = false;
-    for (int w = 0; w < kQ8Warps; ++w) {
-        const WarpPieces x = wp[w];
-        if (x.empty) continue;
-        if (left.first == 3) left.first = 0;
-        if ((x.first || x.last == 2) && ws < 0) {
-            ws = w;
-            before = true;
-        }
-        if (x.first) {
-            join(ws, w, before, true, x.first_seq, x.first_head);
-            ws = -1;
-        }
-        if (x.last == 1) {
-            ws = w;
-            before = false;
         }
     }
-    if (ws >= 0) join(ws, kQ8Warps - 1, before, false, wp[ws].last_seq, wp[ws].last_head);
-    if (tid == 0 && gridDim.x > 1) p.pieces[blockIdx.x] = left;
+    if (tid == 0 && gridDim.x > 1) {
+        CtaPieces left{left_first, left_last, 0, 0, 0, 0, {0, 0}};
+        if (left_last) {
+            const int sg = left_seg >> 16, hh = left_seg & 0xffff;
+            // the share that holds its last unit: a guess good to a share or two, put right
+            const long long last_unit = (long long)P[sg] * Hkv + (long long)(hh + 1) * (P[sg + 1] - P[sg]) - 1;
+            int i = max(0, min((int)((float)last_unit * (float)shares / (float)total), (int)shares - 1));
+            while (share_at(i) > last_unit) --i;
+            while (share_at(i + 1) <= last_unit) ++i;
+            left.end = i / kQ8Warps;
+            left.row0 = kMulti ? row0_of[sg] : sg;
+            left.rows = (kMulti ? n_of[sg] : 1) * group;
+            left.head = hh;
+        }
+        p.pieces[blockIdx.x] = left;
+    }
+    if (!kMulti) {   // rows of empty sequences
+        for (int e = blockIdx.x; e < S; e += gridDim.x)
+            if (lens[e] == 0)
+                for (int i = tid; i < a.num_q_heads * kHeadDim / 8; i += kQ8Threads)
+                    reinterpret_cast<uint4*>(a.out)[(size_t)e * a.num_q_heads * kHeadDim / 8 + i] = make_uint4(0, 0, 0, 0);
+    }
 }
 
-// Joins a segment cut between CTAs: CTA (c, r) takes row r of the segment whose head is CTA c's last
-// piece; the pieces that follow are the first ones of the next CTAs, up to the one that ends it.
-constexpr int kJoinWarps = 4;
+// Joins the segments cut between CTAs: CTA (c, .) takes the segment whose head is CTA c's last piece; the
+// pieces that follow are the first ones of the next CTAs, up to the one that ends it.  A row goes to `split`
+// warps (1, 2, 4 or 8), which share its pieces.  Few registers, so that its CTAs are already resident
+// beside the attention's and only wait for its end.
+constexpr int kJoinWarps = 8;
 
-template <typename T, bool kMulti>
-__global__ void __launch_bounds__(kJoinWarps * 32) q8_join_kernel(const Q8Launch p, int ctas) {
+template <typename T>
+__global__ void __launch_bounds__(kJoinWarps * 32, 5) q8_join_kernel(const Q8Launch p, int ctas, int split) {
     const DecodeQ8Args& a = p.a;
-    __shared__ int end_of;
     __shared__ float4 acc_of[kJoinWarps][32];
     __shared__ float2 ml_of[kJoinWarps];
+    const int c = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int part = warp & (split - 1), r = (blockIdx.y * kJoinWarps + warp) / split;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int c = blockIdx.x, r = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const CtaPieces head = p.pieces[c];
     if (!head.last) return;
-    bool bad;
-    const int L = clamped_len(a.context_lens, head.seq, a.max_blocks_per_seq, a.block_size, &bad);
-    const Seg sg = segment<kMulti>(a, head.seq, head.head, L);
-    const int group = a.num_q_heads / a.num_kv_heads;
-    if (r >= sg.n * group) return;
-    if (threadIdx.x == 0) end_of = ctas - 1;
-    __syncthreads();
-    for (int i = c + 1 + threadIdx.x; i < ctas; i += kJoinWarps * 32)
-        if (p.pieces[i].first < 2) atomicMin(&end_of, i);
-    __syncthreads();
-    const int end = end_of;
+    const int end = min(head.end, ctas - 1), group = a.num_q_heads / a.num_kv_heads;
+    const bool have = r < head.rows;
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kBatch = 8;
-    for (int i0 = c + warp; i0 <= end; i0 += kJoinWarps * kBatch) {
-        float2 ml[kBatch];
-        float4 v[kBatch];
+    constexpr int kBatch = 4;
+    if (have)
+        for (int i0 = c + part; i0 <= end; i0 += split * kBatch) {
+            float2 ml[kBatch];
+            float4 v[kBatch];
+            int some[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int i = i0 + k * kJoinWarps;
-            ml[k] = make_float2(-INFINITY, 0.f);
-            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i <= end && (i == c || p.pieces[i].first != 3)) {
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = min(i0 + k * split, end);
                 const float* piece = p.parts + ((size_t)i * 2 + (i == c ? 1 : 0)) * piece_floats(p.rows);
+                some[k] = p.pieces[i].first;
                 ml[k] = reinterpret_cast<const float2*>(piece + p.rows * kHeadDim)[r];
                 v[k] = *reinterpret_cast<const float4*>(piece + r * kHeadDim + lane * 4);
             }
-        }
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) add_piece(m, l, acc, ml[k], v[k]);
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k * split;
+                if (i <= end && (i == c || some[k] != 3)) add_piece(m, l, acc, ml[k], v[k]);
+            }
+        }
+    if (split > 1) {
+        acc_of[warp][lane] = acc;
+        if (lane == 0) ml_of[warp] = make_float2(m, l);
+        __syncthreads();
+        if (part > 0) return;
+        for (int w = 1; w < split; ++w) add_piece(m, l, acc, ml_of[warp + w], acc_of[warp + w][lane]);
     }
-    acc_of[warp][lane] = acc;
-    if (lane == 0) ml_of[warp] = make_float2(m, l);
-    __syncthreads();
-    if (warp > 0) return;
-    for (int w = 1; w < kJoinWarps; ++w) add_piece(m, l, acc, ml_of[w], acc_of[w][lane]);
-    store_row4<T>(a.out, row_offset(a, sg, group, r) + lane * 4, l, acc);
+    if (have) store_row4<T>(a.out, row_at(a, head.row0, head.head, group, r) + lane * 4, l, acc);
 }
 
 inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
+long long units_bound(int block_size, int max_blocks) {   // of one segment
+    return ((long long)max_blocks * block_size + kTile - 1) / kTile + start_units(kQ8MaxRows);
+}
+
+// Sequences of one launch: their lengths fit on chip, and the units of a kv head in 31 bits.
+int slice_of(int num_seqs, int block_size, int max_blocks) {
+    return (int)max(1LL, min((long long)min(num_seqs, kQ8MaxSeqs), 0x7fffffffLL / units_bound(block_size, max_blocks)));
+}
+
 long long line_bound(int num_seqs, int num_kv_heads, int block_size, int max_blocks) {
-    const long long tiles = ((long long)max_blocks * block_size + kTile - 1) / kTile;
-    return (long long)min(num_seqs, kQ8MaxSeqs) * num_kv_heads * (tiles + kStartUnits);
+    return slice_of(num_seqs, block_size, max_blocks) * num_kv_heads * units_bound(block_size, max_blocks);
 }
 
 // One CTA per SM, fewer for little work: a cut between CTAs costs the joining launch, so a CTA's share
@@ -800,7 +944,11 @@ cudaError_t launch_nt(const Q8Launch& p, int ctas, const CUtensorMap& k, const C
     if (e != cudaSuccess) return e;
     e = launch_pdl(kernel, dim3(ctas), dim3(kQ8Threads), smem, stream, p, k, v);
     if (e != cudaSuccess || ctas == 1) return e;
-    return launch_pdl(q8_join_kernel<T, kMulti>, dim3(ctas - 1, p.rows), dim3(kJoinWarps * 32), 0, stream, p, ctas);
+    // as many warps to a row as a segment has pieces when all are equally long
+    const int pieces = ctas / max(1, min(ctas, p.a.num_seqs * p.a.num_kv_heads));
+    const int split = pieces >= 32 ? 8 : pieces >= 16 ? 4 : pieces >= 8 ? 2 : 1;
+    const int grid_y = (p.rows * split + kJoinWarps - 1) / kJoinWarps;
+    return launch_pdl(q8_join_kernel<T>, dim3(ctas - 1, grid_y), dim3(kJoinWarps * 32), 0, stream, p, ctas, split);
 }
 
 template <typename T, bool kMulti>
@@ -841,10 +989,11 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, int dtype, void* workspace, 
     p.parts = reinterpret_cast<float*>(ws);
     p.firsts = reinterpret_cast<float*>(ws + w.firsts);
     p.pieces = reinterpret_cast<CtaPieces*>(ws + w.pieces);
-    // lengths of kQ8MaxSeqs sequences fit on chip: larger batches go in slices, one after another
-    for (int s0 = 0; s0 < a.num_seqs; s0 += kQ8MaxSeqs) {
+    // larger batches go in slices, one after another
+    const int slice = slice_of(a.num_seqs, a.block_size, a.max_blocks_per_seq);
+    for (int s0 = 0; s0 < a.num_seqs; s0 += slice) {
         p.a = a;
-        p.a.num_seqs = min(kQ8MaxSeqs, a.num_seqs - s0);
+        p.a.num_seqs = min(slice, a.num_seqs - s0);
         p.a.block_tables += (size_t)s0 * a.max_blocks_per_seq;
         p.a.context_lens += s0;
         if (a.q_start) {
