@@ -27,6 +27,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import threading
 from typing import Optional
 
 import numpy as np
@@ -623,14 +624,17 @@ def _device_and_type(name: str, t):
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _call_on(dev: int, stream: Optional[torch.cuda.Stream], name: str, *args) -> None:
-    """The library call with device ``dev`` current, on ``stream`` or dev's current stream."""
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError(f"stream is on {stream.device}, not on cuda:{dev}")
-        raw = stream.cuda_stream
-    else:
-        raw = _current_raw_stream(dev) if _current_raw_stream else torch.cuda.current_stream(dev).cuda_stream
+def _raw_stream(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
+    """``stream``, or device ``dev``'s current stream."""
+    if stream is None:
+        return _current_raw_stream(dev) if _current_raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, not on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _call_on(dev: int, raw: int, name: str, *args) -> None:
+    """The library call on stream ``raw`` of device ``dev``, with dev current."""
     fn = getattr(_native.load(), name)
     if dev == torch.cuda.current_device():
         rc = fn(*args, raw)
@@ -726,7 +730,7 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, in
             ok_ptr, oks = out_k.data_ptr(), Hkv * D
         else:
             ok_ptr, oks = _want_rows("out_k", out_k, q.dtype, dev, k.shape)
-    _call_on(dev, stream, "pa_rope", oq_ptr, ok_ptr, q_ptr, k_ptr, oqs, oks, qs, ks, p_ptr, 8 if wide else 4, f_ptr,
+    _call_on(dev, _raw_stream(dev, stream), "pa_rope", oq_ptr, ok_ptr, q_ptr, k_ptr, oqs, oks, qs, ks, p_ptr, 8 if wide else 4, f_ptr,
              float(magnitude), T, Hq, Hkv, D, 2 * inv_freq.numel(), 1 if interleaved else 0, dt)
     return out_q, out_k
 
@@ -735,10 +739,10 @@ def _q8_cache(k_cache, v_cache, k_exp, v_exp, dev: int):
     """Shape (NB, Hkv, B, D) and the four addresses of an 8-bit cache."""
     ptrs = (_want("k_cache", k_cache, torch.float8_e4m3fn, dev), _want("v_cache", v_cache, torch.float8_e4m3fn, dev),
             _want("k_exp", k_exp, torch.int8, dev), _want("v_exp", v_exp, torch.int8, dev))
-    shape = k_cache.shape
+    shape, exps = k_cache.shape, k_exp.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [NB, Hkv, B, D] alike")
-    if k_exp.shape != shape[:2] or v_exp.shape != k_exp.shape:
+    if len(exps) != 2 or exps[0] != shape[0] or exps[1] != shape[1] or v_exp.shape != exps:
         raise ValueError("k_exp and v_exp must be [NB, Hkv]")
     return shape, ptrs
 
@@ -770,7 +774,7 @@ def cache_append_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
             raise ValueError("query_start must have S + 1 entries")
     elif T != S:
         raise ValueError("without query_start, k and v hold one row per sequence")
-    _call_on(dev, stream, "pa_cache_append_q8", k_ptr, v_ptr, ks, vs, *cache, bt_ptr, cl_ptr, qs_ptr, S, T,
+    _call_on(dev, _raw_stream(dev, stream), "pa_cache_append_q8", k_ptr, v_ptr, ks, vs, *cache, bt_ptr, cl_ptr, qs_ptr, S, T,
              int(max_q) if qs_ptr is not None else 1, Hkv, D, B, NB, block_tables.shape[1], dt)
 
 
@@ -791,7 +795,7 @@ def read_blocks_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Te
     n = src_ids.numel()
     if dst_ids.numel() != n:
         raise ValueError("src_ids and dst_ids must have one length")
-    _call_on(dev, stream, "pa_read_blocks_q8", *cache, NB, dk_ptr, dv_ptr, shape[0], src_ptr, dst_ptr, n, Hkv, D, B, dt)
+    _call_on(dev, _raw_stream(dev, stream), "pa_read_blocks_q8", *cache, NB, dk_ptr, dv_ptr, shape[0], src_ptr, dst_ptr, n, Hkv, D, B, dt)
 
 
 def decode_q8_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
@@ -804,6 +808,23 @@ def decode_q8_workspace_size(num_seqs: int, num_q_heads: int, num_kv_heads: int,
 def _q8_workspace_size(dev: int, *shape) -> int:
     with torch.cuda.device(dev):
         return decode_q8_workspace_size(*shape)
+
+
+_q8_scratch = threading.local()
+
+
+def _q8_workspace(dev: int, raw: int, stream: Optional[torch.cuda.Stream], nbytes: int) -> torch.Tensor:
+    """A workspace whose contents do not matter.  The default stream runs one call after another and cannot be
+    captured, so a host thread keeps one for it per device (another thread's launches may fall between this call's
+    two); on any other stream, and in a graph, a call has its own."""
+    if raw:
+        return _empty_on(stream, (nbytes,), torch.uint8, torch.device("cuda", dev))
+    kept = _q8_scratch.__dict__
+    ws = kept.get(dev)
+    if ws is None or ws.numel() < nbytes:
+        with torch.cuda.stream(torch.cuda.default_stream(dev)):
+            ws = kept[dev] = torch.empty((nbytes,), dtype=torch.uint8, device=torch.device("cuda", dev))
+    return ws
 
 
 def _attention_q8(name, q, k_cache, v_cache, k_exp, v_exp, block_tables, context_lens, query_start, scale,
@@ -830,26 +851,27 @@ def _attention_q8(name, q, k_cache, v_cache, k_exp, v_exp, block_tables, context
     elif T != S:
         raise ValueError("q must hold one row per sequence")
     if out is None:
-        out = _empty_on(stream, (T, Hq, D), q.dtype, q.device)
+        out = torch.empty_like(q) if stream is None else _empty_on(stream, (T, Hq, D), q.dtype, q.device)
         out_ptr = out.data_ptr()
     else:
         out_ptr = _want("out", out, q.dtype, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
+    raw = _raw_stream(dev, stream)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_ptr = _want("workspace", workspace, workspace.dtype, dev)
         ws_bytes = workspace.numel() * workspace.element_size()
     else:
         ws_bytes = _q8_workspace_size(dev, S, Hq, Hkv, D, B, max_blocks, max_q)
-        if ws_bytes:   # of this call alone: its contents before the call do not matter
-            workspace = _empty_on(stream, (ws_bytes,), torch.uint8, q.device)
+        if ws_bytes:
+            workspace = _q8_workspace(dev, raw, stream, ws_bytes)
             ws_ptr = workspace.data_ptr()
     if qs_ptr is None:
-        _call_on(dev, stream, name, out_ptr, q_ptr, *cache, bt_ptr, cl_ptr, float(scale), Hkv, S, Hq, D, B, NB, max_blocks,
+        _call_on(dev, raw, name, out_ptr, q_ptr, *cache, bt_ptr, cl_ptr, float(scale), Hkv, S, Hq, D, B, NB, max_blocks,
                  dt, ws_ptr, ws_bytes)
     else:
-        _call_on(dev, stream, name, out_ptr, q_ptr, *cache, bt_ptr, cl_ptr, qs_ptr, float(scale), Hkv, S, T, max_q, Hq, D,
+        _call_on(dev, raw, name, out_ptr, q_ptr, *cache, bt_ptr, cl_ptr, qs_ptr, float(scale), Hkv, S, T, max_q, Hq, D,
                  B, NB, max_blocks, dt, ws_ptr, ws_bytes)
     return out
 

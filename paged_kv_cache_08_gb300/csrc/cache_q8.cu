@@ -9,11 +9,12 @@
 //   code   = e4m3(x * 2^-e)          to nearest even; beyond 448 (inf, or amax > 448 * 2^60) to +-448
 // The products by a power of two are exact, so a code is off by its own rounding alone.
 //
-// Design: one warp per (touched block, kv head, K or V): it alone decides the block's exponent, so there are
-// no atomics and the result has one value.  It holds 16 rows in registers (32 where a block has 32) and
-// reads those before them again, from L2, once the exponent is known.  The host does not know how many blocks a
-// ragged batch touches; unit v of a sequence is found by a search in the monotone bounds
-// query_start[s] / B + 2 s, which leave every sequence at least the blocks it touches.
+// Design: one warp (2 or 4 for large blocks of long chunks) per (touched block, kv head, K or V): it alone
+// decides the block's exponent, so there are no atomics and the result has one value.  It holds 16 or 32 rows in
+// registers and reads those before them again, from L2, once the exponent is known.  The host does not know how
+// many blocks a ragged batch touches; unit v of a sequence is found by a search in the monotone bounds
+// query_start[s] / B + 2 s, which leave every sequence at least the blocks it touches.  One row per sequence, the
+// decode step's form, has a kernel of its own.
 //
 // read_q8: code * 2^e rounded to the pool's 16-bit type (bf16 exactly), beyond its range to its
 // largest value; one thread per 16 codes of K and of V.  Both are bound by HBM.
@@ -59,13 +60,91 @@ __device__ __forceinline__ uint2 quantise8(const uint4& x, float mul) {
     return make_uint2(w[0], w[1]);
 }
 
-template <typename T, int kRows>
-__global__ void __launch_bounds__(kAppendWarps * 32) append_q8_kernel(const AppendQ8Args a, int blocks) {
+// Eight codes under a grown exponent.
+__device__ __forceinline__ uint2 rescale8(uint2 codes, float down) {
+    const uint32_t w[2] = {codes.x, codes.y};
+    uint32_t n[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float2 p = e4m3x2_to_float2((uint16_t)(w[k] & 0xffffu)), q = e4m3x2_to_float2((uint16_t)(w[k] >> 16));
+        n[k] = (uint32_t)f32_to_e4m3x2(p.x * down, p.y * down) | ((uint32_t)f32_to_e4m3x2(q.x * down, q.y * down) << 16);
+    }
+    return make_uint2(n[0], n[1]);
+}
+
+// One new row per sequence (query_start == null): a warp takes eight kv heads of a sequence, its lower half
+// their K rows and its upper half their V rows, so that the walk from length to table to exponent is made once.
+constexpr int kOneHeads = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(kAppendWarps * 32) append_one_q8_kernel(const AppendQ8Args a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x % 32, c = lane % 16, is_v = lane / 16;
+    const int B = a.block_size, Hkv = a.num_kv_heads, groups = (Hkv + kOneHeads - 1) / kOneHeads;
+    const unsigned u = blockIdx.x * kAppendWarps + threadIdx.x / 32;
+    const int s = (int)(u / groups), h0 = (int)(u % groups) * kOneHeads;
+    if (s >= a.num_seqs) return;
+    const T* src = static_cast<const T*>(is_v ? a.v : a.k) + s * (is_v ? a.v_stride : a.k_stride) + h0 * kHeadDim + c * 8;
+    uint4 x[kOneHeads];
+#pragma unroll
+    for (int i = 0; i < kOneHeads; ++i) {
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (h0 + i < Hkv) x[i] = __ldg(reinterpret_cast<const uint4*>(src + i * kHeadDim));
+    }
+    bool bad_len;
+    const int L = clamped_len(a.context_lens, s, a.max_blocks_per_seq, B, &bad_len);
+    if (bad_len && h0 == 0 && lane == 0) flag_status(a.status, PA_DEV_BAD_CONTEXT);
+    if (L == 0) return;
+    const int blk = __ldg(a.block_tables + (size_t)s * a.max_blocks_per_seq + (L - 1) / B), lo = (L - 1) % B;
+    if (blk < 0 || blk >= a.num_blocks) {
+        if (h0 == 0 && lane == 0) flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
+        return;
+    }
+    const size_t tile0 = (size_t)blk * Hkv + h0;
+    int8_t* exps = (is_v ? a.v_exp : a.k_exp) + tile0;
+    int e_old[kOneHeads];
+#pragma unroll
+    for (int i = 0; i < kOneHeads; ++i) e_old[i] = h0 + i < Hkv ? clamp_exp(exps[i]) : 0;
+#pragma unroll
+    for (int i = 0; i < kOneHeads; ++i) {
+        if (h0 + i >= Hkv) break;
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t m = w[k] & 0x7fff7fffu;
+            top = __vmaxu2(top, m & ~__vcmpgeu2(m, kInf2<T>));   // infinities and NaN do not count
+        }
+        uint32_t amax = max(top & 0xffffu, top >> 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int need = exponent_for(Elem<T>::to_float((uint16_t)amax));
+        const int e = lo == 0 ? need : max(e_old[i], need);
+        uint8_t* dst = (is_v ? a.v_cache : a.k_cache) + (tile0 + i) * B * kHeadDim + c * 8;
+        *reinterpret_cast<uint2*>(dst + lo * kHeadDim) = quantise8<T>(x[i], exp2_int(-e));
+        if (e > e_old[i] && lo > 0) {   // earlier rows: the same values under the grown exponent
+            const float down = exp2_int(e_old[i] - e);
+            for (int r = 0; r < lo; ++r) {
+                uint2* row = reinterpret_cast<uint2*>(dst + r * kHeadDim);
+                *row = rescale8(*row, down);
+            }
+        }
+        if (c == 0) exps[i] = (int8_t)e;
+    }
+}
+
+// kWpu: warps of a unit (0: `warps_per_unit`).
+template <typename T, int kRows, int kWpu>
+__global__ void __launch_bounds__(kAppendWarps * 32) append_q8_kernel(const AppendQ8Args a, int blocks, int warps_per_unit) {
+    const int wpu = kWpu ? kWpu : warps_per_unit;
+    __shared__ uint32_t amax_of[kAppendWarps];
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int B = a.block_size, Hkv = a.num_kv_heads;
-    const unsigned u = blockIdx.x * kAppendWarps + warp;       // (virtual block, head, K or V)
+    const int part = warp % wpu;                               // of the unit's `wpu` warps
+    const unsigned u = blockIdx.x * (kAppendWarps / wpu) + warp / wpu;   // (virtual block, head, K or V)
     const int is_v = u % 2, h = (int)(u / 2 % Hkv), v = (int)(u / 2 / Hkv);
     if (v >= blocks) return;
     int s = v, j = 0;
@@ -76,14 +155,16 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_q8_kernel(const Appe
     bool bad_len;
     const int L = clamped_len(a.context_lens, s, a.max_blocks_per_seq, B, &bad_len);
     const NewRows nr = new_rows(a.q_start, a.rows, a.max_q, s, L);
-    const bool speaks = h == 0 && !is_v && lane == 0;
+    const bool speaks = h == 0 && !is_v && part == 0 && lane == 0;
     if ((bad_len || nr.bad) && j == 0 && speaks) flag_status(a.status, PA_DEV_BAD_CONTEXT);
     const int p0 = L - nr.n;                                   // first new position
     const int blk_i = p0 / B + j;                              // logical block
-    if (j < 0 || nr.n == 0 || blk_i > (L - 1) / B) return;
+    if (j < 0 || nr.n == 0 || blk_i > (L - 1) / B) return;     // (as all of the unit's warps)
     const int blk = __ldg(a.block_tables + (size_t)s * a.max_blocks_per_seq + blk_i);
     const int lo = max(0, p0 - blk_i * B), hi = min(B, L - blk_i * B);   // new rows of the block: [lo, hi)
-    // a batch of rows from b on: this lane has rows b + lane / 16 + 2 i, eight elements (c) of each
+    // a batch of rows from b on: this lane has rows b + lane / 16 + 2 i, eight elements (c) of each; the warp's
+    // batches begin at `begin` and lie `stride_rows` apart
+    const int begin = lo + part * kRows, stride_rows = wpu * kRows;
     const int c = lane % 16;
     const long long stride = is_v ? a.v_stride : a.k_stride;
     const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (nr.row0 + (long long)(blk_i * B - p0)) * stride +
@@ -97,7 +178,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_q8_kernel(const Appe
             if (r < hi) x[i] = __ldg(reinterpret_cast<const uint4*>(src + r * stride));
         }
     };
-    load(lo);
+    load(begin);
     if (blk < 0 || blk >= a.num_blocks) {
         if (speaks) flag_status(a.status, PA_DEV_BAD_BLOCK_ID);
         return;
@@ -107,7 +188,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_q8_kernel(const Appe
     const int e_old = clamp_exp(exps[tile]);
     // the largest magnitude, in the type's bits (their order is the values')
     uint32_t top = 0;
-    int b = lo;   // the batch held
+    int b = begin;   // the batch held
     for (;;) {
         uint32_t t = top;
 #pragma unroll
@@ -129,13 +210,18 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_q8_kernel(const Appe
         } else {
             top = t;
         }
-        if (b + kRows >= hi) break;
-        b += kRows;
+        if (b + stride_rows >= hi) break;
+        b += stride_rows;
         load(b);
     }
     uint32_t amax = max(top & 0xffffu, top >> 16);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (wpu > 1) {
+        if (lane == 0) amax_of[warp] = amax;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpu), "r"(wpu * 32) : "memory");
+        for (int i = warp - part; i < warp - part + wpu; ++i) amax = max(amax, amax_of[i]);
+    }
     const int need = exponent_for(Elem<T>::to_float((uint16_t)amax));   // (every lane has read the old exponent)
     const int e = lo == 0 ? need : max(e_old, need);
     uint8_t* dst = (is_v ? a.v_cache : a.k_cache) + tile * B * kHeadDim + c * 8;
@@ -146,28 +232,19 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_q8_kernel(const Appe
             const int r = b + lane / 16 + 2 * i;
             if (r < hi) *reinterpret_cast<uint2*>(dst + r * kHeadDim) = quantise8<T>(x[i], mul);
         }
-        if (b == lo) break;
-        b -= kRows;
+        if (b == begin) break;
+        b -= stride_rows;
         load(b);
     }
     if (e > e_old && lo > 0) {
         // earlier rows: the same values under the grown exponent
         const float down = exp2_int(e_old - e);
-        for (int r = lane / 16; r < lo; r += 2) {
-            const uint2 old = *reinterpret_cast<const uint2*>(dst + r * kHeadDim);
-            const uint32_t w[2] = {old.x, old.y};
-            uint32_t n[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float2 p = e4m3x2_to_float2((uint16_t)(w[k] & 0xffffu));
-                const float2 q = e4m3x2_to_float2((uint16_t)(w[k] >> 16));
-                n[k] = (uint32_t)f32_to_e4m3x2(p.x * down, p.y * down) |
-                       ((uint32_t)f32_to_e4m3x2(q.x * down, q.y * down) << 16);
-            }
-            *reinterpret_cast<uint2*>(dst + r * kHeadDim) = make_uint2(n[0], n[1]);
+        for (int r = part * 2 + lane / 16; r < lo; r += 2 * wpu) {
+            uint2* row = reinterpret_cast<uint2*>(dst + r * kHeadDim);
+            *row = rescale8(*row, down);
         }
     }
-    if (lane == 0) exps[tile] = (int8_t)e;
+    if (part == 0 && lane == 0) exps[tile] = (int8_t)e;
 }
 
 // Two fp32 to two 16-bit values, to nearest; beyond the type's range to its largest value, NaN stays.
@@ -223,11 +300,22 @@ __global__ void __launch_bounds__(256) read_q8_kernel(const ReadQ8Args a) {
 
 template <typename T>
 static cudaError_t launch_append(const AppendQ8Args& a, cudaStream_t stream) {
-    const int blocks = a.q_start ? a.rows / a.block_size + 2 * a.num_seqs : a.num_seqs;
+    const dim3 block(kAppendWarps * 32);
+    if (!a.q_start) {
+        const long long warps = (long long)a.num_seqs * ((a.num_kv_heads + kOneHeads - 1) / kOneHeads);
+        return launch_pdl(append_one_q8_kernel<T>, dim3((unsigned)((warps + kAppendWarps - 1) / kAppendWarps)), block, 0,
+                          stream, a);
+    }
+    const int blocks = a.rows / a.block_size + 2 * a.num_seqs;
+    // 64- and 128-row blocks of long chunks: 2 or 4 warps hold the rows in registers (one pass); of few rows: one
+    // warp, whose idle neighbours would only fill the SMs
+    const int wpu = a.block_size > 32 && a.rows / a.num_seqs >= a.block_size / 2 ? a.block_size / 32 : 1;
     const long long units = 2LL * blocks * a.num_kv_heads;
-    const dim3 grid((unsigned)((units + kAppendWarps - 1) / kAppendWarps)), block(kAppendWarps * 32);
-    return a.block_size == 32 ? launch_pdl(append_q8_kernel<T, 32>, grid, block, 0, stream, a, blocks)
-                              : launch_pdl(append_q8_kernel<T, 16>, grid, block, 0, stream, a, blocks);
+    const int per_cta = kAppendWarps / wpu;
+    const dim3 grid((unsigned)((units + per_cta - 1) / per_cta));
+    if (wpu > 1) return launch_pdl(append_q8_kernel<T, 32, 0>, grid, block, 0, stream, a, blocks, wpu);
+    return a.block_size == 32 ? launch_pdl(append_q8_kernel<T, 32, 1>, grid, block, 0, stream, a, blocks, 1)
+                              : launch_pdl(append_q8_kernel<T, 16, 1>, grid, block, 0, stream, a, blocks, 1);
 }
 
 cudaError_t launch_append_q8(const AppendQ8Args& a, int dtype, cudaStream_t stream) {

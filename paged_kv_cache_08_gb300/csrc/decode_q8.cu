@@ -105,19 +105,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Products and transposes without side effects, which the compiler may move freely among loads and
-// conversions (two warps a scheduler: each has to overlap its own latencies).
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
 }
 
 __device__ __forceinline__ uint32_t lo_f16x2(uint32_t w) { return e4m3x2_to_f16x2((uint16_t)(w & 0xffffu)); }
@@ -248,8 +241,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     float base[NT][2], sum[NT][2];
     // of this lane's score columns (rows 2 t and 2 t + 1 of each 8): the factor to log2 units and the last
     // position the row sees; with Q in shared memory these are kept there too
-    float qf_reg[M::kQInSmem ? 1 : NT][2];
-    int lim_reg[M::kQInSmem ? 1 : NT][2];
+    float qf_reg[M::kQInSmem ? 1 : NT][2] = {};
+    int lim_reg[M::kQInSmem ? 1 : NT][2] = {};
     float2* qf_sm = reinterpret_cast<float2*>(smem + M::kOffCol) + warp * M::kRows;          // [NT][4] factors,
     int2* lim_sm = reinterpret_cast<int2*>(qf_sm + M::kRows / 2);                            // [NT][4] limits
     auto qf_of = [&](int nt) {
@@ -360,25 +353,20 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     };
 
     // One tile of tokens t0 .. t0 + 15 against the first K x 8 rows.
-    auto run_tile = [&](auto kc, uint32_t tile_at, int t0, int ke, int ve) {
+    auto run_tile = [&](auto kc, uint32_t tile, int t0, int ke, int ve) {
         constexpr int K = decltype(kc)::value;
-        const uint8_t* tile = smem + tile_at;
-        const uint4 k0 = *reinterpret_cast<const uint4*>(tile + k_off0), k1 = *reinterpret_cast<const uint4*>(tile + k_off1);
-        const uint4 k2 = *reinterpret_cast<const uint4*>(tile + k_off0 + 1024);
-        const uint4 k3 = *reinterpret_cast<const uint4*>(tile + k_off1 + 1024);
-        uint4 v0 = *reinterpret_cast<const uint4*>(tile + v_off0), v1 = *reinterpret_cast<const uint4*>(tile + v_off1);
-        uint4 v2 = *reinterpret_cast<const uint4*>(tile + v_off0 + 1024);
-        uint4 v3 = *reinterpret_cast<const uint4*>(tile + v_off1 + 1024);
         // S = K Q^T
-        float sc[K][4];
+        float x[K][4];
         {
+            const uint4 k0 = lds128(tile + k_off0), k1 = lds128(tile + k_off1);
+            const uint4 k2 = lds128(tile + k_off0 + 1024), k3 = lds128(tile + k_off1 + 1024);
             const uint32_t ka[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
             const uint32_t kb[8] = {k2.x, k2.y, k2.z, k2.w, k3.x, k3.y, k3.z, k3.w};
-            float odd[K == 1 ? 1 : K][4];   // one tile of rows: odd steps on their own, for two short chains
+            float y[K][4];   // one tile of rows: odd steps on their own, for two short chains
 #pragma unroll
             for (int nt = 0; nt < K; ++nt)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) sc[nt][c] = odd[nt][c] = 0.f;
+                for (int c = 0; c < 4; ++c) x[nt][c] = y[nt][c] = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint4 b[K];
@@ -393,45 +381,42 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     const uint32_t a0 = lo_f16x2(ka[2 * q]), a1 = lo_f16x2(kb[2 * q]), a2 = hi_f16x2(ka[2 * q]),
                                    a3 = hi_f16x2(kb[2 * q]);
 #pragma unroll
-                    for (int nt = 0; nt < K; ++nt) mma_f16(sc[nt], a0, a1, a2, a3, b[nt].x, b[nt].y);
+                    for (int nt = 0; nt < K; ++nt) mma16816<__half>(x[nt], a0, a1, a2, a3, b[nt].x, b[nt].y);
                 }
                 {
                     const uint32_t a0 = lo_f16x2(ka[2 * q + 1]), a1 = lo_f16x2(kb[2 * q + 1]),
                                    a2 = hi_f16x2(ka[2 * q + 1]), a3 = hi_f16x2(kb[2 * q + 1]);
 #pragma unroll
-                    for (int nt = 0; nt < K; ++nt) mma_f16(K == 1 ? odd[nt] : sc[nt], a0, a1, a2, a3, b[nt].z, b[nt].w);
+                    for (int nt = 0; nt < K; ++nt)
+                        mma16816<__half>(K == 1 ? y[nt] : x[nt], a0, a1, a2, a3, b[nt].z, b[nt].w);
                 }
             }
             if (K == 1) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) sc[0][c] += odd[0][c];
+                for (int c = 0; c < 4; ++c) x[0][c] += y[0][c];
             }
         }
+        uint4 v0 = lds128(tile + v_off0), v1 = lds128(tile + v_off1);
+        uint4 v2 = lds128(tile + v_off0 + 1024), v3 = lds128(tile + v_off1 + 1024);
 
-        // x = score in log2 units + ve - base; positions a row does not see to -inf
+        // x = score in log2 units + ve; positions a row does not see to -inf
         const float ks = exp2_int(ke), vef = (float)ve, unscale = exp2_int(-ve);
         const bool masked = t0 + kTile > p0 + 1;
         bool nan_v = false;
-        float x[K][4];
-        auto scores = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < K; ++nt) {
+            const float2 qf = qf_of(nt);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(x[nt][c], (c & 1 ? qf.y : qf.x) * ks, vef);
+        }
+        if (masked) {
 #pragma unroll
             for (int nt = 0; nt < K; ++nt) {
-                const float2 qf = qf_of(nt);
+                const int2 lim = lim_of(nt);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(sc[nt][c], (c & 1 ? qf.y : qf.x) * ks, vef - base[nt][c & 1]);
+                for (int c = 0; c < 4; ++c)
+                    if (t0 + g + (c >> 1) * 8 > (c & 1 ? lim.y : lim.x)) x[nt][c] = -INFINITY;
             }
-            if (masked) {
-#pragma unroll
-                for (int nt = 0; nt < K; ++nt) {
-                    const int2 lim = lim_of(nt);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (t0 + g + (c >> 1) * 8 > (c & 1 ? lim.y : lim.x)) x[nt][c] = -INFINITY;
-                }
-            }
-        };
-        scores();
-        if (masked) {
             // rows behind the last token hold anything: zero codes
             const int left = L - t0;
             if (2 * t >= left) v0 = make_uint4(0, 0, 0, 0);
@@ -457,26 +442,20 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 }
             }
         }
-        float top = x[0][0];   // NaN does not move a base
+        bool move = false;   // a column without a base yet (-inf) takes one as soon as it sees a token
 #pragma unroll
         for (int nt = 0; nt < K; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) top = fmaxf(top, x[nt][c]);
-        // a column without a base yet (-inf) has +inf here as soon as it sees a token
-        if (__any_sync(kAll, top > kBaseSlack)) {
+            for (int c = 0; c < 2; ++c) move |= fmaxf(x[nt][c], x[nt][c + 2]) > base[nt][c] + kBaseSlack;
+        if (__any_sync(kAll, move)) {
 #pragma unroll
-            for (int nt = 0; nt < K; ++nt) {
-                const float2 qf = qf_of(nt);
-                const int2 lim = lim_of(nt);
+            for (int nt = 0; nt < K; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float f1 = (c ? qf.y : qf.x) * ks;
-                    const int last = c ? lim.y : lim.x;
-                    float m = base[nt][c];
-                    if (!masked || t0 + g <= last) m = fmaxf(m, fmaf(sc[nt][c], f1, vef));
-                    if (!masked || t0 + g + 8 <= last) m = fmaxf(m, fmaf(sc[nt][c + 2], f1, vef));
+                    float m = fmaxf(x[nt][c], x[nt][c + 2]);
 #pragma unroll
                     for (int k = 4; k < 32; k <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
+                    m = fmaxf(m, base[nt][c]);
                     const float f = base[nt][c] == -INFINITY ? 0.f : ex2(base[nt][c] - m);
                     base[nt][c] = m;
                     sum[nt][c] *= f;
@@ -486,19 +465,23 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                         o[nt][k][c + 2] *= f;
                     }
                 }
-            }
-            scores();
         }
         uint32_t b0[K], b1[K];
 #pragma unroll
         for (int nt = 0; nt < K; ++nt) {
             float pr[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) pr[c] = ex2(x[nt][c]);
+            for (int c = 0; c < 4; ++c) pr[c] = ex2(x[nt][c] - base[nt][c & 1]);
+            if (masked) {   // a row without a base yet has -inf - -inf here
+                const int2 lim = lim_of(nt);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (t0 + g + (c >> 1) * 8 > (c & 1 ? lim.y : lim.x)) pr[c] = 0.f;
+            }
             sum[nt][0] = fmaf(pr[0] + pr[2], unscale, sum[nt][0]);
             sum[nt][1] = fmaf(pr[1] + pr[3], unscale, sum[nt][1]);
-            b0[nt] = transpose8x8(Elem<__half>::pack2(pr[0], pr[1]));
-            b1[nt] = transpose8x8(Elem<__half>::pack2(pr[2], pr[3]));
+            b0[nt] = movmatrix_trans(Elem<__half>::pack2(pr[0], pr[1]));
+            b1[nt] = movmatrix_trans(Elem<__half>::pack2(pr[2], pr[3]));
         }
         // O += V^T P^T
         const uint32_t va[4] = {v0.x, v0.y, v0.z, v0.w}, vb[4] = {v1.x, v1.y, v1.z, v1.w};
@@ -511,13 +494,13 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 const uint32_t ab = __byte_perm(va[q], vb[q], sel), cd = __byte_perm(vc[q], vd[q], sel);
                 const uint32_t a0 = lo_f16x2(ab), a1 = hi_f16x2(ab), a2 = lo_f16x2(cd), a3 = hi_f16x2(cd);
 #pragma unroll
-                for (int nt = 0; nt < K; ++nt) mma_f16(o[nt][2 * q + e], a0, a1, a2, a3, b0[nt], b1[nt]);
+                for (int nt = 0; nt < K; ++nt) mma16816<__half>(o[nt][2 * q + e], a0, a1, a2, a3, b0[nt], b1[nt]);
             }
         }
         if (kMulti && nan_v) {
             // rare: NaN into the dims and rows that see such a token
             for (int j = 0; j < min(kTile, L - t0); ++j) {
-                const uint4 v = *reinterpret_cast<const uint4*>(tile + kTileHalf + j * 128 + ((g ^ (j & 7)) << 4));
+                const uint4 v = lds128(tile + kTileHalf + j * 128 + ((uint32_t)(g ^ (j & 7)) << 4));
                 const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int d = 0; d < 16; ++d)
@@ -680,7 +663,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     dead = __any_sync(kAll, dead);
                     if (dead) break;
                     phases ^= 1u << st;
-                    const uint32_t tile = warp * M::kRing + st * kTileBytes;
+                    const uint32_t tile = ring + st * kTileBytes;
                     const int t0 = (r - kStartUnits) * kTile;
                     if (!kMulti || NT == 1) {
                         run_tile(std::integral_constant<int, NT>{}, tile, t0, ke, ve);

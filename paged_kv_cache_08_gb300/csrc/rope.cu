@@ -10,9 +10,9 @@
 // p * F_i modulo 2^64 is the reduced angle, exact by integer wrap-around (negative positions too).
 // The error is that of F_i, p * 2^-65 turns beside f_i's own in fp64.
 //
-// Design: a CTA takes one to eight tokens.  Its threads first work out the tokens' R/2 cosines and sines once
+// Design: a CTA takes one to 16 tokens, so that the grid is whole waves.  Its threads first work out the tokens' R/2 cosines and sines once
 // (shared by all heads), with the first vectors of the heads already on their way, then each thread turns
-// 16-byte vectors, four in flight.  The work is bound by HBM: every element is read and written once.
+// 16-byte vectors of one column of the heads, two in flight.  The work is bound by HBM: every element is read and written once.
 #include "q8.cuh"
 
 namespace pa {
@@ -20,8 +20,9 @@ namespace pa {
 namespace {
 
 constexpr int kRopeThreads = 256;   // 128 where one vector per thread is enough
-constexpr int kRopeBatch = 4;       // vectors (pairs of vectors) of a thread in flight
-constexpr int kRopeTokens = 8;      // tokens of a CTA at most
+constexpr int kRopeBatch = 2;       // vectors (pairs of vectors) of a thread in flight
+constexpr int kRopePerSm = 5;       // CTAs (of 256 threads, 51 registers) per SM
+constexpr int kRopeTokens = 16;     // tokens of a CTA at most
 
 __device__ __forceinline__ uint64_t turns64(double f) {
     const double t = f * 0.15915494309189533577;   // 1 / (2 pi)
@@ -45,94 +46,116 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return u;
 }
 
-// Vector `i` of a CTA's work: its token, its head's first vectors, and its index in the head: the turned
-// vectors first (pairs of vectors in the half layout), then those passed on.
-struct Item {
-    const uint4* in;
-    uint4* out;
-    int t, v;
-    bool keep;   // passed on in place: nothing to do
-};
-
-template <typename T>
-__device__ __forceinline__ Item item_at(const RopeArgs& a, unsigned t0, unsigned i, unsigned per_head, unsigned turned) {
-    const unsigned heads = a.num_q_heads + a.num_kv_heads;
-    const unsigned th = i / per_head, t = th / heads, h = th - t * heads, v = i - th * per_head;
-    const bool is_q = h < (unsigned)a.num_q_heads;
-    const unsigned at = (is_q ? h : h - a.num_q_heads) * (a.head_dim / 8);
-    const long long tok = t0 + t;
-    return Item{reinterpret_cast<const uint4*>(static_cast<const T*>(is_q ? a.q : a.k) + tok * (is_q ? a.q_stride : a.k_stride)) + at,
-                reinterpret_cast<uint4*>(static_cast<T*>(is_q ? a.out_q : a.out_k) + tok * (is_q ? a.out_q_stride : a.out_k_stride)) + at,
-                (int)t, (int)v, v >= turned && (is_q ? a.in_place_q : a.in_place_k)};
-}
-
 template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a, int tokens) {
-    extern __shared__ float2 cs[];   // [tokens][R / 2] cos, sin (magnitude included)
+__global__ void __launch_bounds__(kRopeThreads, kRopePerSm) rope_kernel(const RopeArgs a, int tokens) {
+    extern __shared__ float4 cs4[];   // [tokens][R / 2] (cos, sin), magnitude included
+    float2* cs = reinterpret_cast<float2*>(cs4);
     grid_dependency_wait();
     grid_launch_dependents();
     const int t0 = blockIdx.x * tokens, n = min(tokens, a.num_tokens - t0);
-    const int pairs = a.rotary_dim / 2;
+    const int pairs = a.rotary_dim / 2, vecs = a.head_dim / 8, heads = a.num_q_heads + a.num_kv_heads;
     const int rot = a.rotary_dim / 8, half = rot / 2, turned = kInterleaved ? rot : half;
-    const int rest = rot - turned;   // where the vectors passed on begin, less `turned`
-    const int per_head = turned + a.head_dim / 8 - rot;
-    const int items = n * (a.num_q_heads + a.num_kv_heads) * per_head;
-    uint4 x[kRopeBatch], y[kInterleaved ? 1 : kRopeBatch];
-    auto load = [&](int i0) {
-#pragma unroll
-        for (int k = 0; k < kRopeBatch; ++k) {
-            const int i = i0 + k * blockDim.x;
-            if (i < items) {
-                const Item it = item_at<T>(a, t0, i, per_head, turned);
-                x[k] = it.in[it.v >= turned ? it.v + rest : it.v];
-                if (!kInterleaved && it.v < turned) y[kInterleaved ? 0 : k] = it.in[it.v + half];
+    // A thread keeps to one column of the heads: a turned vector (two, one of each half, in the half layout), or
+    // one that is passed on; of the CTA's heads, token after token, it takes every `step`-th.
+    const int columns = turned + vecs - rot, step = max(1, (int)blockDim.x / columns);
+    const int first = threadIdx.x / columns, step_t = step / heads, step_h = step - step_t * heads;
+    for (int col = threadIdx.x - first * columns, pass = 0; pass * (int)blockDim.x < columns; ++pass, col += blockDim.x) {
+        const bool works = columns > (int)blockDim.x ? col < columns : first < step;
+        const bool turns = col < turned;
+        const int at = turns ? col : col + rot - turned;
+        struct Cursor {
+            int t, h;
+        };
+        auto next = [&](Cursor& c) {
+            c.h += step_h;
+            c.t += step_t;
+            if (c.h >= heads) {
+                c.h -= heads;
+                ++c.t;
             }
-        }
-    };
-    load(threadIdx.x);   // on their way while the angles are worked out
-    for (int i = threadIdx.x; i < n * pairs; i += blockDim.x) {
-        const int t = i / pairs, f = i - t * pairs;
-        const long long p = a.wide_positions ? static_cast<const long long*>(a.positions)[t0 + t]
-                                             : (long long)static_cast<const int32_t*>(a.positions)[t0 + t];
-        const float2 w = cos_sin((uint64_t)p * turns64(a.inv_freq[f]));
-        cs[i] = make_float2(w.x * a.magnitude, w.y * a.magnitude);
-    }
-    __syncthreads();
-    for (int i0 = threadIdx.x;;) {
+        };
+        auto in_of = [&](const Cursor& c) {
+            const long long t = t0 + c.t;
+            return (c.h < a.num_q_heads
+                        ? reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + t * a.q_stride) + c.h * vecs
+                        : reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + t * a.k_stride) + (c.h - a.num_q_heads) * vecs) + at;
+        };
+        auto out_of = [&](const Cursor& c) {
+            const long long t = t0 + c.t;
+            return (c.h < a.num_q_heads
+                        ? reinterpret_cast<uint4*>(static_cast<T*>(a.out_q) + t * a.out_q_stride) + c.h * vecs
+                        : reinterpret_cast<uint4*>(static_cast<T*>(a.out_k) + t * a.out_k_stride) + (c.h - a.num_q_heads) * vecs) + at;
+        };
+        Cursor from{works ? first / heads : n, first % heads}, to = from;
+        uint4 x[kRopeBatch], y[kInterleaved ? 1 : kRopeBatch];
+        auto load = [&]() {
 #pragma unroll
-        for (int k = 0; k < kRopeBatch; ++k) {
-            const int i = i0 + k * blockDim.x;
-            if (i >= items) break;
-            const Item it = item_at<T>(a, t0, i, per_head, turned);
-            if (it.v >= turned) {
-                if (!it.keep) it.out[it.v + rest] = x[k];
-            } else if (kInterleaved) {   // four pairs
-                float f[8], r[8];
-                unpack8<T>(x[k], f);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 w = cs[it.t * pairs + it.v * 4 + j];
-                    r[2 * j] = f[2 * j] * w.x - f[2 * j + 1] * w.y;
-                    r[2 * j + 1] = f[2 * j + 1] * w.x + f[2 * j] * w.y;
+            for (int k = 0; k < kRopeBatch; ++k) {
+                if (from.t < n) {
+                    const uint4* src = in_of(from);
+                    x[k] = src[0];
+                    if (!kInterleaved && turns) y[kInterleaved ? 0 : k] = src[half];
+                    next(from);
                 }
-                it.out[it.v] = pack8<T>(r);
-            } else {                     // eight pairs, a vector of each half
-                float f[8], g[8], rf[8], rg[8];
-                unpack8<T>(x[k], f);
-                unpack8<T>(y[kInterleaved ? 0 : k], g);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 w = cs[it.t * pairs + it.v * 8 + j];
-                    rf[j] = f[j] * w.x - g[j] * w.y;
-                    rg[j] = g[j] * w.x + f[j] * w.y;
-                }
-                it.out[it.v] = pack8<T>(rf);
-                it.out[it.v + half] = pack8<T>(rg);
             }
+        };
+        load();   // on their way while the angles are worked out
+        if (pass == 0) {
+            // a thread keeps to one pair (its frequency costs five fp64 operations) and takes tokens in turn
+            const int lanes = min(pairs, (int)blockDim.x), groups = blockDim.x / lanes, group = threadIdx.x / lanes;
+            if (group < groups)
+                for (int f = threadIdx.x - group * lanes; f < pairs; f += lanes) {
+                    const uint64_t turn = turns64(a.inv_freq[f]);
+                    for (int t = group; t < n; t += groups) {
+                        const long long p = a.wide_positions ? static_cast<const long long*>(a.positions)[t0 + t]
+                                                             : (long long)static_cast<const int32_t*>(a.positions)[t0 + t];
+                        const float2 w = cos_sin((uint64_t)p * turn);
+                        cs[t * pairs + f] = make_float2(w.x * a.magnitude, w.y * a.magnitude);
+                    }
+                }
+            __syncthreads();
         }
-        i0 += kRopeBatch * blockDim.x;
-        if (i0 >= items) break;
-        load(i0);
+        while (to.t < n) {
+#pragma unroll
+            for (int k = 0; k < kRopeBatch; ++k) {
+                if (to.t < n) {
+                    uint4* dst = out_of(to);
+                    if (!turns) {
+                        if (!(to.h < a.num_q_heads ? a.in_place_q : a.in_place_k)) dst[0] = x[k];
+                    } else if (kInterleaved) {   // four pairs
+                        const float4* w4 = cs4 + (to.t * pairs + col * 4) / 2;
+                        float f[8], r[8];
+                        unpack8<T>(x[k], f);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float4 w = w4[j];
+                            r[4 * j] = f[4 * j] * w.x - f[4 * j + 1] * w.y;
+                            r[4 * j + 1] = f[4 * j + 1] * w.x + f[4 * j] * w.y;
+                            r[4 * j + 2] = f[4 * j + 2] * w.z - f[4 * j + 3] * w.w;
+                            r[4 * j + 3] = f[4 * j + 3] * w.z + f[4 * j + 2] * w.w;
+                        }
+                        dst[0] = pack8<T>(r);
+                    } else {                     // eight pairs, a vector of each half
+                        const float4* w4 = cs4 + (to.t * pairs + col * 8) / 2;
+                        float f[8], g[8], rf[8], rg[8];
+                        unpack8<T>(x[k], f);
+                        unpack8<T>(y[kInterleaved ? 0 : k], g);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 w = w4[j];
+                            rf[2 * j] = f[2 * j] * w.x - g[2 * j] * w.y;
+                            rg[2 * j] = g[2 * j] * w.x + f[2 * j] * w.y;
+                            rf[2 * j + 1] = f[2 * j + 1] * w.z - g[2 * j + 1] * w.w;
+                            rg[2 * j + 1] = g[2 * j + 1] * w.z + f[2 * j + 1] * w.w;
+                        }
+                        dst[0] = pack8<T>(rf);
+                        dst[half] = pack8<T>(rg);
+                    }
+                    next(to);
+                }
+            }
+            load();
+        }
     }
 }
 
@@ -141,8 +164,9 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a,
 template <typename T>
 static cudaError_t launch_type(const RopeArgs& a, cudaStream_t stream) {
     const int rot = a.rotary_dim / 8, per_head = (a.interleaved ? rot : rot / 2) + a.head_dim / 8 - rot;
-    // as many tokens to a CTA as leave four CTAs to every SM, eight at most
-    const int tokens = max(1, min(kRopeTokens, a.num_tokens / (4 * sm_count_current())));
+    // whole waves of CTAs, each CTA with at most kRopeTokens tokens
+    const int slots = kRopePerSm * sm_count_current(), waves = (a.num_tokens + slots * kRopeTokens - 1) / (slots * kRopeTokens);
+    const int tokens = (a.num_tokens + slots * waves - 1) / (slots * waves);
     const bool small = tokens * (a.num_q_heads + a.num_kv_heads) * per_head <= 128;
     const dim3 grid((unsigned)((a.num_tokens + tokens - 1) / tokens)), block(small ? 128 : kRopeThreads);
     const size_t smem = (size_t)tokens * (a.rotary_dim / 2) * sizeof(float2);
