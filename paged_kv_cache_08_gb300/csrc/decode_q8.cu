@@ -66,6 +66,8 @@ struct Q8Launch {
     float* firsts;        // [grid * warps] pieces, when they do not fit in shared memory
     CtaPieces* pieces;    // [grid]
     int rows;             // query rows of a segment at most (max_q * group)
+    int group;            // query heads per kv head
+    unsigned group_inv;   // ceil(2^16 / group)
 };
 
 template <int NT>
@@ -138,9 +140,13 @@ __device__ __forceinline__ void store_row4(void* out, size_t at, float l, const 
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = w;
 }
 
+// Query token of row r of a segment, r / group for r < 32, by the multiplier that p.group_inv holds.
+__device__ __forceinline__ int token_of(const Q8Launch& p, int r) { return (int)((unsigned)r * p.group_inv >> 16); }
+
 // Element of query row r (token r / group, group member r % group) of kv head h's segment.
-__device__ __forceinline__ size_t row_at(const DecodeQ8Args& a, int row0, int h, int group, int r) {
-    return ((size_t)(row0 + r / group) * a.num_q_heads + (size_t)h * group + r % group) * kHeadDim;
+__device__ __forceinline__ size_t row_at(const Q8Launch& p, int row0, int h, int r) {
+    const int i = token_of(p, r);
+    return ((size_t)(row0 + i) * p.a.num_q_heads + (size_t)h * p.group + r - i * p.group) * kHeadDim;
 }
 
 // In a piece in shared memory, 16-byte chunk c of row r lies at c ^ (r / 2 % 4): the lanes that store
@@ -178,7 +184,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     grid_launch_dependents();
 
     // ---- lengths, and the units of one kv head before each sequence (P) ----
-    const int S = a.num_seqs, Hkv = a.num_kv_heads, group = a.num_q_heads / Hkv;
+    const int S = a.num_seqs, Hkv = a.num_kv_heads, group = p.group;
     {
         __shared__ int warp_sum_of[kQ8Warps];
         int carry = 0;
@@ -261,7 +267,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     auto load_q = [&](int s, int h, int nt, uint4 (&to)[4]) {
         const int first = kMulti ? row0_of[s] : s, rows = (kMulti ? n_of[s] : 1) * group, r = nt * 8 + g;
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                          row_at(a, first, h, group, r < rows ? r : 0) + 32 * t);
+                                                          row_at(p, first, h, r < rows ? r : 0) + 32 * t);
 #pragma unroll
         for (int i = 0; i < 4; ++i) to[i] = r < rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
     };
@@ -329,7 +335,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int col = nt * 8 + 2 * t + c;
-                lim[c] = kMulti && col < nrows ? p0 + col / group : L - 1;
+                lim[c] = kMulti && col < nrows ? p0 + token_of(p, col) : L - 1;
                 base[nt][c] = -INFINITY;
                 sum[nt][c] = 0.f;
             }
@@ -554,7 +560,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     uint32_t w[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) w[i] = Elem<T>::pack2(o[nt][i][c] * inv, o[nt][i][c + 2] * inv);
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row_at(a, row0, h, group, r) +
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row_at(p, row0, h, r) +
                                                           g * 16);
                     dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                     dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -788,7 +794,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 const int r = r0 + i;
                 if (r < rows) {
                     if (closed && !before) {
-                        store_row4<T>(a.out, row_at(a, first, hh, group, r) + lane * 4, li, acc[i]);
+                        store_row4<T>(a.out, row_at(p, first, hh, r) + lane * 4, li, acc[i]);
                     } else {
                         *reinterpret_cast<float4*>(to + r * kHeadDim + lane * 4) = acc[i];
                         if (lane == 0) reinterpret_cast<float2*>(to + p.rows * kHeadDim)[r] = make_float2(mi, li);
@@ -838,7 +844,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 5) q8_join_kernel(const Q8Lau
     grid_launch_dependents();
     const CtaPieces head = p.pieces[c];
     if (!head.last) return;
-    const int end = min(head.end, ctas - 1), group = a.num_q_heads / a.num_kv_heads;
+    const int end = min(head.end, ctas - 1);
     const bool have = r < head.rows;
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -869,29 +875,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 5) q8_join_kernel(const Q8Lau
         if (part > 0) return;
         for (int w = 1; w < split; ++w) add_piece(m, l, acc, ml_of[warp + w], acc_of[warp + w][lane]);
     }
-    if (have) store_row4<T>(a.out, row_at(a, head.row0, head.head, group, r) + lane * 4, l, acc);
+    if (have) store_row4<T>(a.out, row_at(p, head.row0, head.head, r) + lane * 4, l, acc);
 }
 
 inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
-long long units_bound(int block_size, int max_blocks) {   // of one segment
-    return ((long long)max_blocks * block_size + kTile - 1) / kTile + start_units(kQ8MaxRows);
+long long units_bound(int block_size, int max_blocks, int rows) {   // of one segment
+    return ((long long)max_blocks * block_size + kTile - 1) / kTile + start_units((rows + 7) / 8 * 8);
 }
 
 // Sequences of one launch: their lengths fit on chip, and the units of a kv head in 31 bits.
-int slice_of(int num_seqs, int block_size, int max_blocks) {
-    return (int)max(1LL, min((long long)min(num_seqs, kQ8MaxSeqs), 0x7fffffffLL / units_bound(block_size, max_blocks)));
+int slice_of(int num_seqs, int block_size, int max_blocks, int rows) {
+    return (int)max(1LL, min((long long)min(num_seqs, kQ8MaxSeqs), 0x7fffffffLL / units_bound(block_size, max_blocks, rows)));
 }
 
-long long line_bound(int num_seqs, int num_kv_heads, int block_size, int max_blocks) {
-    return slice_of(num_seqs, block_size, max_blocks) * num_kv_heads * units_bound(block_size, max_blocks);
+long long line_bound(int num_seqs, int num_kv_heads, int block_size, int max_blocks, int rows) {
+    return slice_of(num_seqs, block_size, max_blocks, rows) * num_kv_heads * units_bound(block_size, max_blocks, rows);
 }
 
-// One CTA per SM, fewer for little work: a cut between CTAs costs the joining launch, so a CTA's share
-// is at least four tiles a warp of the longest contexts the tables allow.
-int q8_ctas(int num_seqs, int num_kv_heads, int block_size, int max_blocks) {
-    const long long want = (line_bound(num_seqs, num_kv_heads, block_size, max_blocks) + 4 * kQ8Warps - 1) / (4 * kQ8Warps);
-    return (int)max(1LL, min(want, (long long)sm_count_current()));
+// One CTA per SM, fewer for little work: a cut between CTAs costs the joining launch (2.5 us), so at the longest
+// contexts the tables allow one CTA takes up to eight units a warp alone, and several take four at least.
+int q8_ctas(int num_seqs, int num_kv_heads, int block_size, int max_blocks, int rows) {
+    const long long units = line_bound(num_seqs, num_kv_heads, block_size, max_blocks, rows);
+    if (units <= 8 * kQ8Warps) return 1;
+    return (int)min((units + 4 * kQ8Warps - 1) / (4 * kQ8Warps), (long long)sm_count_current());
 }
 
 struct Q8Layout {
@@ -949,14 +956,14 @@ cudaError_t launch_rows(const Q8Launch& p, int ctas, const CUtensorMap& k, const
 size_t q8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int max_q, int block_size,
                           int max_blocks_per_seq) {
     if (num_seqs == 0) return 0;
-    const int ctas = q8_ctas(num_seqs, num_kv_heads, block_size, max_blocks_per_seq);
     const int rows = num_q_heads / num_kv_heads * max_q;
+    const int ctas = q8_ctas(num_seqs, num_kv_heads, block_size, max_blocks_per_seq, rows);
     return ctas == 1 && rows <= 16 ? 0 : q8_layout(ctas, rows).bytes;
 }
 
 bool q8_line_fits(int num_seqs, int num_kv_heads, int block_size, int max_blocks_per_seq) {
-    const int ctas = q8_ctas(num_seqs, num_kv_heads, block_size, max_blocks_per_seq);
-    return line_bound(num_seqs, num_kv_heads, block_size, max_blocks_per_seq) / (ctas * kQ8Warps) < (1LL << 30);
+    const int ctas = q8_ctas(num_seqs, num_kv_heads, block_size, max_blocks_per_seq, kQ8MaxRows);
+    return line_bound(num_seqs, num_kv_heads, block_size, max_blocks_per_seq, kQ8MaxRows) / (ctas * kQ8Warps) < (1LL << 30);
 }
 
 cudaError_t launch_decode_q8(const DecodeQ8Args& a, int dtype, void* workspace, cudaStream_t stream) {
@@ -965,15 +972,17 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, int dtype, void* workspace, 
     if (!encode_q8_map(a.k_cache, pool_rows, &k) || !encode_q8_map(a.v_cache, pool_rows, &v))
         return cudaErrorInvalidValue;
     Q8Launch p;
-    p.rows = a.num_q_heads / a.num_kv_heads * a.max_q;
-    const int ctas = q8_ctas(a.num_seqs, a.num_kv_heads, a.block_size, a.max_blocks_per_seq);
+    p.group = a.num_q_heads / a.num_kv_heads;
+    p.group_inv = (65536u + p.group - 1) / p.group;
+    p.rows = p.group * a.max_q;
+    const int ctas = q8_ctas(a.num_seqs, a.num_kv_heads, a.block_size, a.max_blocks_per_seq, p.rows);
     const Q8Layout w = q8_layout(ctas, p.rows);
     char* ws = static_cast<char*>(workspace);
     p.parts = reinterpret_cast<float*>(ws);
     p.firsts = reinterpret_cast<float*>(ws + w.firsts);
     p.pieces = reinterpret_cast<CtaPieces*>(ws + w.pieces);
     // larger batches go in slices, one after another
-    const int slice = slice_of(a.num_seqs, a.block_size, a.max_blocks_per_seq);
+    const int slice = slice_of(a.num_seqs, a.block_size, a.max_blocks_per_seq, p.rows);
     for (int s0 = 0; s0 < a.num_seqs; s0 += slice) {
         p.a = a;
         p.a.num_seqs = min(slice, a.num_seqs - s0);
