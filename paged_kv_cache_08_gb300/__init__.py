@@ -573,8 +573,23 @@ def gather_runs(src_k: torch.Tensor, src_v: torch.Tensor, dst_k: torch.Tensor, d
 # rotary positions and the 8-bit cache
 # ------------------------------------------------------------------------------------------
 
-# These calls are short on the GPU (microseconds), so their checks touch each tensor once: its type, device
-# and layout together, with the message worked out only when one is wrong.
+# These calls are short on the GPU (microseconds).  Their common case (plain tensors on the current device, the
+# current stream) is checked and passed on in C (csrc/marshal.c), which returns None when a call is any other:
+# the code below then takes it.  It touches each tensor once, its type, device and layout together, and works out
+# the message only when one is wrong.
+
+_marshal = None
+
+
+def _in_c():
+    global _marshal
+    if _marshal is None:
+        m = _native.load_marshal()
+        m.setup(torch.Tensor, (torch.float16, torch.bfloat16, torch.float8_e4m3fn, torch.int8, torch.int32, torch.int64,
+                               torch.float64), torch.empty_like, _raw_stream_of, torch.cuda.current_device,
+                _q8_workspace)
+        _marshal = m
+    return _marshal
 
 def _want(name: str, t, dtype, dev: int) -> int:
     """The address of a contiguous tensor of ``dtype`` on CUDA device ``dev``."""
@@ -621,13 +636,15 @@ def _device_and_type(name: str, t):
     return t.get_device(), dt
 
 
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# handle of a device's current stream (2.8 us by way of a torch.cuda.Stream)
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream",
+                         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _raw_stream(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
     """``stream``, or device ``dev``'s current stream."""
     if stream is None:
-        return _current_raw_stream(dev) if _current_raw_stream else torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream_of(dev)
     if stream.device.index != dev:
         raise ValueError(f"stream is on {stream.device}, not on cuda:{dev}")
     return stream.cuda_stream
@@ -700,6 +717,10 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, in
     ``inv_freq``: float64 [R / 2] (see rope_frequencies); the first R elements of each head are turned, as
     pairs (i, i + R/2) or, ``interleaved``, (2i, 2i + 1).  out_q = q and out_k = k turn them in place.
     Token strides are free (slices of a fused projection).  Returns (out_q, out_k).  See pa_rope."""
+    if stream is None:
+        both = (_marshal or _in_c()).rope(q, k, positions, inv_freq, magnitude, interleaved, out_q, out_k)
+        if both is not None:
+            return both
     dev, dt = _device_and_type("q", q)
     q_ptr, qs = _want_rows("q", q, q.dtype, dev)
     T, Hq, D = q.shape
@@ -755,6 +776,9 @@ def cache_append_q8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     query_start[s+1]-1 are sequence s's newest tokens (at most ``max_q``), or without query_start row s
     is sequence s's newest token.  Updates the caches and the exponents of the blocks written.  Token
     strides of k and v are free.  See pa_cache_append_q8."""
+    if stream is None and (_marshal or _in_c()).append(k, v, k_cache, v_cache, k_exp, v_exp, block_tables, context_lens,
+                                                       query_start, max_q):
+        return
     dev, dt = _device_and_type("k", k)
     (NB, Hkv, B, D), cache = _q8_cache(k_cache, v_cache, k_exp, v_exp, dev)
     k_ptr, ks = _want_rows("k", k, k.dtype, dev)
@@ -783,6 +807,9 @@ def read_blocks_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_exp: torch.Te
                    stream: Optional[torch.cuda.Stream] = None) -> None:
     """Blocks back to 16 bits: dst[dst_ids[i]] = the values of block src_ids[i] (int32 ids; pools dst_k, dst_v
     [NBd, Hkv, B, 128] float16 or bfloat16).  See pa_read_blocks_q8."""
+    if stream is None and (_marshal or _in_c()).read_blocks(k_cache, v_cache, k_exp, v_exp, dst_k, dst_v, src_ids,
+                                                            dst_ids):
+        return
     dev, dt = _device_and_type("dst_k", dst_k)
     (NB, Hkv, B, D), cache = _q8_cache(k_cache, v_cache, k_exp, v_exp, dev)
     dk_ptr = _want("dst_k", dst_k, dst_k.dtype, dev)
@@ -829,6 +856,11 @@ def _q8_workspace(dev: int, raw: int, stream: Optional[torch.cuda.Stream], nbyte
 
 def _attention_q8(name, q, k_cache, v_cache, k_exp, v_exp, block_tables, context_lens, query_start, scale,
                   num_kv_heads, max_q, out, workspace, stream) -> torch.Tensor:
+    if stream is None and workspace is None:
+        done = (_marshal or _in_c()).attention(q, k_cache, v_cache, k_exp, v_exp, block_tables, context_lens, query_start,
+                                               scale, num_kv_heads, max_q, out)
+        if done is not None:
+            return done
     dev, dt = _device_and_type("q", q)
     q_ptr = _want("q", q, q.dtype, dev)
     (NB, Hkv, B, D), cache = _q8_cache(k_cache, v_cache, k_exp, v_exp, dev)

@@ -7,11 +7,14 @@ shared library is missing, loading raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import re
 from pathlib import Path
 
 _PKG = Path(__file__).resolve().parent
 LIB_PATH = _PKG / "_build" / "libpa.so"
+MARSHAL_PATH = _PKG / "_build" / "_marshal.so"
 HEADER = _PKG.parent / "include" / "pa.h"
 
 c_int, c_i64, c_u64, c_size, c_f32, c_vp = (ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t,
@@ -136,6 +139,18 @@ def load() -> ctypes.CDLL:
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+def load_marshal():
+    """The binding's C part (csrc/marshal.c), which calls libpa.so without ctypes."""
+    load()
+    if not MARSHAL_PATH.exists():
+        raise RuntimeError(f"_marshal.so not built ({MARSHAL_PATH}); run `python -m paged_kv_cache_08_gb300.build` "
+                           "or __graft_entry__.build() first")
+    loader = importlib.machinery.ExtensionFileLoader("_marshal", str(MARSHAL_PATH))
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+    loader.exec_module(module)
+    return module
 
 
 class PAError(RuntimeError):

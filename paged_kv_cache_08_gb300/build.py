@@ -1,4 +1,4 @@
-"""Build libpa.so (CUDA kernels + C ABI + host pool) for sm_103a, in-tree.
+"""Build libpa.so (CUDA kernels + C ABI + host pool) for sm_103a and the binding's C part, in-tree.
 
     python -m paged_kv_cache_08_gb300.build [--force]
 
@@ -10,6 +10,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -19,6 +20,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = BUILD / "libpa.so"
+MARSHAL = BUILD / "_marshal.so"
 
 CUDA_SOURCES = ["api.cu", "api_q8.cu", "cache_q8.cu", "cache_write.cu", "copy_blocks.cu", "decode_fma.cu", "decode_mma.cu",
                 "decode_persist.cu", "decode_planned.cu", "decode_q8.cu", "decode_static.cu",
@@ -73,6 +75,17 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> Path:
         if r.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    src = CSRC / "marshal.c"
+    if force or not MARSHAL.exists() or MARSHAL.stat().st_mtime < max(src.stat().st_mtime, hdr):
+        tmp = BUILD / f"_marshal.so.tmp{os.getpid()}"
+        cmd = ["gcc", "-O2", "-fPIC", "-shared", "-Wall", "-I", sysconfig.get_paths()["include"], str(src), "-o", str(tmp),
+               "-L", str(BUILD), "-lpa", "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        if r.stderr.strip():
+            sys.stderr.write(r.stderr)
+        os.replace(tmp, MARSHAL)
     return LIB
 
 

@@ -28,6 +28,7 @@
 //       the tokens of a dim.  P^T comes from S by movmatrix.
 // The base moves only when a score exceeds it by 2^8 (then O and l are rescaled), so most tiles need
 // no shuffle.  Bound by HBM (one byte per cached element).
+#include <atomic>
 #include <type_traits>
 
 #include "decode_common.cuh"
@@ -930,8 +931,16 @@ template <typename T, int NT, bool kMulti>
 cudaError_t launch_nt(const Q8Launch& p, int ctas, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
     constexpr size_t smem = 1024 + Q8Smem<NT>::kBytes;
     auto kernel = q8_attend_kernel<T, NT, kMulti>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
+    static std::atomic<unsigned long long> allowed{0};   // devices on which the kernel may have its shared memory
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev > 63 || !(allowed.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        allowed.fetch_or(dev > 63 ? 0 : bit);
+    }
     e = launch_pdl(kernel, dim3(ctas), dim3(kQ8Threads), smem, stream, p, k, v);
     if (e != cudaSuccess || ctas == 1) return e;
     // as many warps to a row as a segment has pieces when all are equally long
