@@ -6,12 +6,14 @@
 // with K_t, V_t the codes of token t and ke, ve its block's exponents.  Tokens of a block whose table
 // entry lies outside the pool are left out.
 //
-// The exponents cost one add each: with x_t = scale log2(e) 2^ke (q . K_t) + ve and a base b,
-//   P_t = 2^(x_t - b),  O = sum P_t V_t (codes),  l = sum P_t 2^-ve,  out = O / l,
-// so V is never scaled, P_t stays in fp16's range whatever the blocks' scales (the base follows the
-// maximum of x_t, not of the score), and b cancels.  Codes become fp16 exactly; P is rounded to fp16
-// for the PV product (2^-11 of a weight, averaged over the tokens; fp32 sums).  bf16 queries are scaled
-// by a power of two per row into fp16's range (exact down to 2^-29 of the row's largest element).
+// The exponents cost a product each: with x_t = scale log2(e) 2^ke (q . K_t) and a base b,
+//   p_t = 2^(x_t - b),  P_t = p_t 2^ve,  O = sum P_t V_t (codes),  l = sum p_t,  out = O / l,
+// so V is never scaled, P_t stays in fp16's range whatever the blocks' scales (the base follows the maximum
+// of x_t + ve, not of the score), and b cancels.  p_t keeps the weights' sum: between blocks of scales 2^-60 and
+// 2^60 it spans 2^-68 .. 2^68 where it counts, inside fp32 (factors between bases may be subnormal: exp2f).
+// Codes become fp16 exactly; P is rounded to fp16 for the PV product (2^-11 of a weight, averaged over the
+// tokens; fp32 sums).  bf16 queries are scaled by a power of two per row into fp16's range (exact down to
+// 2^-29 of the row's largest element).
 //
 // Work split: a segment is a (sequence, kv head); its 16-token tiles and one unit for its start lie on a
 // line, segment after segment, and every warp of the grid takes an equal, contiguous share of the line.
@@ -122,7 +124,7 @@ __device__ __forceinline__ uint32_t hi_f16x2(uint32_t w) { return e4m3x2_to_f16x
 // (m, l, acc) of one row joined with a piece; a piece that saw no token has base -inf.
 __device__ __forceinline__ void add_piece(float& m, float& l, float4& acc, float2 ml, float4 v) {
     const float m2 = fmaxf(m, ml.x);
-    const float f0 = m == -INFINITY ? 0.f : ex2(m - m2), f1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - m2);
+    const float f0 = m == -INFINITY ? 0.f : exp2f(m - m2), f1 = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m2);
     m = m2;
     l = l * f0 + ml.y * f1;
     acc.x = acc.x * f0 + v.x * f1;
@@ -406,15 +408,15 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         uint4 v0 = lds128(tile + v_off0), v1 = lds128(tile + v_off1);
         uint4 v2 = lds128(tile + v_off0 + 1024), v3 = lds128(tile + v_off1 + 1024);
 
-        // x = score in log2 units + ve; positions a row does not see to -inf
-        const float ks = exp2_int(ke), vef = (float)ve, unscale = exp2_int(-ve);
+        // x = score in log2 units; positions a row does not see to -inf
+        const float ks = exp2_int(ke), vs = exp2_int(ve), vef = (float)ve, slack = kBaseSlack - vef;
         const bool masked = t0 + kTile > p0 + 1;
         bool nan_v = false;
 #pragma unroll
         for (int nt = 0; nt < K; ++nt) {
             const float2 qf = qf_of(nt);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) x[nt][c] = fmaf(x[nt][c], (c & 1 ? qf.y : qf.x) * ks, vef);
+            for (int c = 0; c < 4; ++c) x[nt][c] *= (c & 1 ? qf.y : qf.x) * ks;
         }
         if (masked) {
 #pragma unroll
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
 #pragma unroll
         for (int nt = 0; nt < K; ++nt)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) move |= fmaxf(x[nt][c], x[nt][c + 2]) > base[nt][c] + kBaseSlack;
+            for (int c = 0; c < 2; ++c) move |= fmaxf(x[nt][c], x[nt][c + 2]) > base[nt][c] + slack;
         if (__any_sync(kAll, move)) {
 #pragma unroll
             for (int nt = 0; nt < K; ++nt)
@@ -462,8 +464,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     float m = fmaxf(x[nt][c], x[nt][c + 2]);
 #pragma unroll
                     for (int k = 4; k < 32; k <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
-                    m = fmaxf(m, base[nt][c]);
-                    const float f = base[nt][c] == -INFINITY ? 0.f : ex2(base[nt][c] - m);
+                    m = fmaxf(m + vef, base[nt][c]);
+                    const float f = base[nt][c] == -INFINITY ? 0.f : exp2f(base[nt][c] - m);
                     base[nt][c] = m;
                     sum[nt][c] *= f;
 #pragma unroll
@@ -485,10 +487,10 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 for (int c = 0; c < 4; ++c)
                     if (t0 + g + (c >> 1) * 8 > (c & 1 ? lim.y : lim.x)) pr[c] = 0.f;
             }
-            sum[nt][0] = fmaf(pr[0] + pr[2], unscale, sum[nt][0]);
-            sum[nt][1] = fmaf(pr[1] + pr[3], unscale, sum[nt][1]);
-            b0[nt] = movmatrix_trans(Elem<__half>::pack2(pr[0], pr[1]));
-            b1[nt] = movmatrix_trans(Elem<__half>::pack2(pr[2], pr[3]));
+            sum[nt][0] += pr[0] + pr[2];
+            sum[nt][1] += pr[1] + pr[3];
+            b0[nt] = movmatrix_trans(Elem<__half>::pack2(pr[0] * vs, pr[1] * vs));
+            b1[nt] = movmatrix_trans(Elem<__half>::pack2(pr[2] * vs, pr[3] * vs));
         }
         // O += V^T P^T
         const uint32_t va[4] = {v0.x, v0.y, v0.z, v0.w}, vb[4] = {v1.x, v1.y, v1.z, v1.w};
@@ -766,7 +768,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             float m = ml.x;
 #pragma unroll
             for (int k = 1; k < kQ8Warps; k <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
-            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+            const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
             float l = f * ml.y;
 #pragma unroll
             for (int k = 1; k < kQ8Warps; k <<= 1) l += __shfl_xor_sync(kAll, l, k);
@@ -978,8 +980,14 @@ bool q8_line_fits(int num_seqs, int num_kv_heads, int block_size, int max_blocks
 cudaError_t launch_decode_q8(const DecodeQ8Args& a, int dtype, void* workspace, cudaStream_t stream) {
     CUtensorMap k, v;
     const unsigned long long pool_rows = (unsigned long long)a.num_blocks * a.num_kv_heads * a.block_size;
-    if (!encode_q8_map(a.k_cache, pool_rows, &k) || !encode_q8_map(a.v_cache, pool_rows, &v))
-        return cudaErrorInvalidValue;
+    if (!encode_q8_map(a.k_cache, pool_rows, &k)) {
+        // a host thread that has made no CUDA call yet has no current context, which the encoding asks for
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess ||
+            !encode_q8_map(a.k_cache, pool_rows, &k))
+            return cudaErrorInvalidValue;
+    }
+    if (!encode_q8_map(a.v_cache, pool_rows, &v)) return cudaErrorInvalidValue;
     Q8Launch p;
     p.group = a.num_q_heads / a.num_kv_heads;
     p.group_inv = (65536u + p.group - 1) / p.group;

@@ -70,7 +70,8 @@ def _tables(lens, block, nb, seed):
 
 
 @pytest.mark.parametrize("block", [16, 32, 64, 128])
-@pytest.mark.parametrize("heads,dtype", [(1, torch.float16), (3, torch.bfloat16), (8, torch.float16)])
+@pytest.mark.parametrize("heads,dtype", [(1, torch.float16), (3, torch.bfloat16), (8, torch.float16),
+                                         (9, torch.bfloat16), (20, torch.float16)])
 def test_append_one_row_each(block, heads, dtype):
     lens = [1, 2, 0, block - 1, block, block + 1, 2 * block, 3 * block + 7, 5]
     c = Cache(40, heads, block, seed=block)
@@ -89,6 +90,20 @@ def test_append_ragged(block, dtype):
     c = Cache(80, 2, block, seed=3)
     k, v = _rows(int(start[-1]), 2, dtype, seed=4)
     c.append(k, v, _tables(lens, block, 80, 5), lens, start, max_q=300)
+    c.check()
+    assert pa.read_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("block", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_append_long_chunks(block, dtype):
+    """Chunks of several blocks, begun and ended inside one."""
+    lens, new = [300, 470], [299, 390]
+    start = np.array([0, 299, 689])
+    c = Cache(64, 3, block, seed=33)
+    k, v = _rows(689, 3, dtype, seed=34)
+    k[5, 1, 3], v[400, 2, 100], k[688, 0, 0] = float("inf"), float("nan"), 3e4
+    c.append(k, v, _tables(lens, block, 64, 35), lens, start, max_q=400)
     c.check()
     assert pa.read_device_status(clear=True) == 0
 
@@ -221,6 +236,29 @@ def test_append_in_a_graph_and_on_a_stream():
         c.check()
         lens.add_(1)
         k.mul_(1.5)
+
+
+def test_every_way_to_call_gives_the_same():
+    """By way of the binding's C part, and of its Python code (a stream, a tensor of another class)."""
+    k, v = _rows(4, 2, torch.float16, seed=36)
+    tables, lens = np.arange(12, dtype=np.int32).reshape(4, 3), [17, 5, 32, 1]
+    c = Cache(12, 2, 16, seed=37)
+    start = [x.clone() for x in c.dev]
+    c.append(k, v, tables, lens)
+    c.check()
+    for how in (dict(stream=torch.cuda.current_stream()), dict(q=torch.arange(5, dtype=torch.int32, device=DEV)),
+                dict(k=torch.nn.Parameter(k, requires_grad=False))):
+        again = [x.clone() for x in start]
+        pa.cache_append_q8(how.get("k", k), v, *again, *c.args[:2], query_start=how.get("q"), max_q=2,
+                           stream=how.get("stream"))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(again, c.dev))
+    ids = torch.arange(12, dtype=torch.int32, device=DEV)
+    outs = [[torch.empty((12, 2, 16, ref.D), dtype=torch.bfloat16, device=DEV) for _ in range(2)] for _ in range(2)]
+    pa.read_blocks_q8(*c.dev, *outs[0], ids, ids)
+    pa.read_blocks_q8(*c.dev, *outs[1], ids, ids, stream=torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(*outs))
 
 
 # ---- read-back -----------------------------------------------------------------------------

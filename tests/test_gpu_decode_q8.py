@@ -142,6 +142,19 @@ def test_exponents_at_their_limits():
     p.run(2.0 ** -60)
 
 
+@pytest.mark.parametrize("scale", [0.3, 1.0, 3.0])
+def test_values_of_extreme_blocks_far_apart_in_score(scale):
+    """V blocks 2^120 apart whose tokens share the weight: the sum of weights keeps the small blocks' tokens,
+    within a piece, when the base moves, and when pieces meet."""
+    for lens, block, seed in (([900, 64, 33], 16, 0), ([6000, 700], 128, 1)):
+        p = Problem(lens, 6, 1, block, torch.bfloat16, seed=166 + seed, spread=0.0)
+        p.exps[1][:] = np.where(np.arange(p.exps[1].size).reshape(p.exps[1].shape) % 2, -60, 60)
+        p.run(scale)
+        p.exps[1][:] = 60
+        p.exps[1][p.tables[0, 0]] = -60
+        p.run(scale)
+
+
 def test_nan_is_where_the_definition_has_it():
     """A NaN in V reaches its dimension in the rows that see its token; one in K every dimension of them."""
     p = Problem([40, 50, 33], 4, 2, 16, torch.float16, new=[6, 4, 8], seed=68)
@@ -182,6 +195,39 @@ def test_queries_at_bf16s_limits(top):
         p.run(2.0 ** -108)
     else:
         p.run(1.0)
+
+
+@pytest.mark.parametrize("new", [None, [5, 1, 0, 3]])
+def test_tables_much_wider_than_the_contexts(new):
+    """The grid is sized by the table's width: most shares are then empty, or a unit or two."""
+    for lens in ([5, 60, 7, 33], [5, 0, 7, 3]):
+        n = None if new is None else [min(a, b) for a, b in zip(new, lens)]
+        p = Problem(lens, 12, 2, 16, torch.float16, new=n, seed=96)
+        p.tables = np.concatenate([p.tables, np.full((4, 3000), -1, dtype=np.int32)], axis=1)
+        p.run()
+
+
+@pytest.mark.parametrize("group,n", [(4, 4), (8, 3), (4, 8), (1, 32), (16, 2)])
+def test_several_tokens_over_long_contexts(group, n):
+    """Segments cut between warps and CTAs with 9 to 32 rows."""
+    Problem([3000, 40, 777], group, 1, 32, torch.float16, new=[n, 2, n], seed=97).run()
+
+
+def test_several_tokens_of_many_sequences():
+    rng = np.random.default_rng(98)
+    lens = rng.integers(0, 30, 1100)
+    new = np.minimum(lens, rng.integers(0, 3, 1100))
+    Problem(lens.tolist(), 2, 1, 16, torch.float16, new=new.tolist(), seed=98).run()
+
+
+def test_no_sequences_and_no_rows():
+    p = Problem([20, 33], 4, 1, 16, torch.float16, new=[0, 0], seed=99)
+    p.upload()
+    assert p.call().shape == (0, 4, 128)
+    p.args[5], p.args[6], p.args[7] = p.args[5][:0], p.args[6][:0], p.args[7][:1]
+    assert p.call().shape == (0, 4, 128)
+    q, kc, vc, ke, ve, t, n, _ = p.args
+    assert pa.decode_q8(q, kc, vc, ke, ve, t, n, SCALE, 1).shape == (0, 4, 128)
 
 
 def test_bad_blocks_are_left_out():
@@ -276,6 +322,47 @@ def test_streams_do_not_share_scratch():
                 g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(w, o) for w, o in zip(want, outs))
+
+
+def test_two_host_threads_on_one_stream():
+    import threading
+    ps = [Problem([2500 + 700 * i, 90], 6, 1, 16, torch.float16, seed=88 + i) for i in range(3)]
+    want = [p.run() for p in ps]
+    got = [[] for _ in ps]
+
+    def work(i):
+        for _ in range(60):
+            got[i].append(ps[i].call())
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert len(g) == 60 and all(torch.equal(w, x) for x in g)
+
+
+def test_every_way_to_call_gives_the_same():
+    """The C part of the binding takes plain tensors on the current stream; a stream, a workspace, or a tensor of
+    another class goes by way of Python."""
+    for new in (None, [3, 1]):
+        p = Problem([400, 33], 12, 2, 16, torch.float16, new=new, seed=92)
+        want = p.run()
+        ws = torch.empty(pa.decode_q8_workspace_size(2, 12, 2, 128, 16, p.tables.shape[1], p.max_q) + 16,
+                         dtype=torch.uint8, device=DEV)
+        out = torch.empty_like(want)
+        assert torch.equal(p.call(stream=torch.cuda.current_stream()), want)
+        assert torch.equal(p.call(workspace=ws), want)
+        assert torch.equal(p.call(workspace=ws, out=out, stream=torch.cuda.current_stream()), want)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            assert torch.equal(p.call(), want)
+        torch.cuda.synchronize()
+        p.args[0] = torch.nn.Parameter(p.args[0], requires_grad=False)
+        assert torch.equal(p.call(), want)
 
 
 def test_a_captured_call_follows_lengths_and_tables():

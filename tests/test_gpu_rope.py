@@ -133,6 +133,37 @@ def test_rope_on_a_stream_and_in_a_graph():
     _check(out[0], q, pos + 17, f, m, False)
 
 
+def test_rope_every_way_to_call_gives_the_same():
+    q, k, pos = _inputs(21, 12, 2, 128, torch.float16, seed=19, fused=True)
+    p = pos.to(DEV)
+    f, m = pa.rope_frequencies(64)
+    want = pa.rope(q, k, p, f)
+    _check(want[0], q, pos, f, m, False)
+    assert want[0].is_contiguous() and want[1].is_contiguous()
+    got = [pa.rope(q, k, p, f, stream=torch.cuda.current_stream()), pa.rope(q, k, p.int(), f),
+           pa.rope(torch.nn.Parameter(q, requires_grad=False), k, p, f),
+           (pa.rope(q, None, p, f)[0], pa.rope(k, None, p, f)[0])]
+    outs = torch.empty((21, 14, 128), dtype=torch.float16, device=DEV)
+    pa.rope(q, k, p, f, out_q=outs[:, :12], out_k=outs[:, 12:])
+    torch.cuda.synchronize()
+    for a, b in got + [(outs[:, :12], outs[:, 12:])]:
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+def test_rope_beyond_32_bit_offsets():
+    T, H = 530000, 32                                 # 2.17e9 elements
+    x = torch.zeros((T, H, 128), dtype=torch.bfloat16, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(21)
+    x[-3:] = torch.randn((3, H, 128), generator=gen, device=DEV)
+    pos = torch.arange(T, device=DEV)
+    f, m = pa.rope_frequencies(128)
+    before = x[-3:].clone()
+    pa.rope(x, None, pos, f, out_q=x)
+    torch.cuda.synchronize()
+    _check(x[-3:], before, pos[-3:].cpu(), f, m, False)
+    assert not x[:-3].any()
+
+
 def test_rope_refuses():
     q, k, pos = _inputs(4, 2, 1, 128, torch.float16, seed=17)
     p = pos.to(DEV)
