@@ -845,26 +845,31 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 5) q8_join_kernel(const Q8Lau
     const int part = warp & (split - 1), r = (blockIdx.y * kJoinWarps + warp) / split;
     grid_dependency_wait();
     grid_launch_dependents();
+    constexpr int kBatch = 4;
+    float2 ml[kBatch];
+    float4 v[kBatch];
+    int some[kBatch];
+    auto load = [&](int i0, int end) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = min(i0 + k * split, end);
+            const float* piece = p.parts + ((size_t)i * 2 + (i == c ? 1 : 0)) * piece_floats(p.rows);
+            some[k] = p.pieces[i].first;
+            ml[k] = reinterpret_cast<const float2*>(piece + p.rows * kHeadDim)[r];
+            v[k] = *reinterpret_cast<const float4*>(piece + r * kHeadDim + lane * 4);
+        }
+    };
+    // the first pieces are read before it is known whether they are the segment's: one round trip less
+    if (r < p.rows) load(c + part, ctas - 1);
     const CtaPieces head = p.pieces[c];
     if (!head.last) return;
     const int end = min(head.end, ctas - 1);
     const bool have = r < head.rows;
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kBatch = 4;
     if (have)
         for (int i0 = c + part; i0 <= end; i0 += split * kBatch) {
-            float2 ml[kBatch];
-            float4 v[kBatch];
-            int some[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int i = min(i0 + k * split, end);
-                const float* piece = p.parts + ((size_t)i * 2 + (i == c ? 1 : 0)) * piece_floats(p.rows);
-                some[k] = p.pieces[i].first;
-                ml[k] = reinterpret_cast<const float2*>(piece + p.rows * kHeadDim)[r];
-                v[k] = *reinterpret_cast<const float4*>(piece + r * kHeadDim + lane * 4);
-            }
+            if (i0 != c + part) load(i0, end);
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int i = i0 + k * split;

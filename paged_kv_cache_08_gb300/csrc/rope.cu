@@ -165,10 +165,11 @@ template <typename T>
 static cudaError_t launch_type(const RopeArgs& a, cudaStream_t stream) {
     const int rot = a.rotary_dim / 8, per_head = (a.interleaved ? rot : rot / 2) + a.head_dim / 8 - rot;
     // whole waves of CTAs, each CTA with at most kRopeTokens tokens
-    const int slots = kRopePerSm * sm_count_current(), waves = (a.num_tokens + slots * kRopeTokens - 1) / (slots * kRopeTokens);
-    const int tokens = (a.num_tokens + slots * waves - 1) / (slots * waves);
+    const long long slots = kRopePerSm * sm_count_current(), most = slots * kRopeTokens;
+    const long long waves = (a.num_tokens + most - 1) / most;
+    const int tokens = (int)((a.num_tokens + slots * waves - 1) / (slots * waves));
     const bool small = tokens * (a.num_q_heads + a.num_kv_heads) * per_head <= 128;
-    const dim3 grid((unsigned)((a.num_tokens + tokens - 1) / tokens)), block(small ? 128 : kRopeThreads);
+    const dim3 grid((unsigned)(((long long)a.num_tokens + tokens - 1) / tokens)), block(small ? 128 : kRopeThreads);
     const size_t smem = (size_t)tokens * (a.rotary_dim / 2) * sizeof(float2);
     return a.interleaved ? launch_pdl(rope_kernel<T, true>, grid, block, smem, stream, a, tokens)
                          : launch_pdl(rope_kernel<T, false>, grid, block, smem, stream, a, tokens);
