@@ -40,8 +40,10 @@ namespace pa {
 
 namespace {
 
-constexpr int kQ8Warps = 8;
-constexpr int kQ8Threads = kQ8Warps * 32;
+// Warps of a CTA.  12 where a warp begins and ends several short segments, whose waits the others fill (256 short
+// chats of 32 heads 62 -> 57 us); 8 elsewhere, with deeper rings and fewer streams (16 contexts of 16384 tokens
+// 90 -> 85 us).
+constexpr int kFewWarps = 8, kManyWarps = 12;
 constexpr int kTile = 16;                       // tokens per tile
 constexpr uint32_t kTileHalf = kTile * kHeadDim;   // 2 KB of K, 2 KB of V
 constexpr uint32_t kTileBytes = 2 * kTileHalf;
@@ -73,20 +75,20 @@ struct Q8Launch {
     unsigned group_inv;   // ceil(2^16 / group)
 };
 
-template <int NT>
+template <int NT, int kW>
 struct Q8Smem {
-    static constexpr int kRows = NT * 8;
+    static constexpr int kRows = NT * 8, kWarps = kW, kThreads = kWarps * 32;
     static constexpr bool kQInSmem = NT >= 3;              // Q fragments (16 registers per 8 rows) leave the registers
     static constexpr bool kFirstInSmem = NT <= 2;
-    static constexpr int kStages = NT == 1 ? 5 : 4;
+    static constexpr int kStages = kW > kFewWarps ? 3 : NT == 1 ? 5 : 4;
     static constexpr uint32_t kRing = kStages * kTileBytes;  // per warp
-    static constexpr uint32_t kOffFirst = kQ8Warps * kRing;
-    static constexpr uint32_t kOffLastMl = kOffFirst + (kFirstInSmem ? kQ8Warps * piece_floats(kRows) * 4 : 0);
-    static constexpr uint32_t kOffQ = kOffLastMl + kQ8Warps * kRows * 8;
-    static constexpr uint32_t kOffCol = kOffQ + (kQInSmem ? kQ8Warps * NT * 16 * 32 * 4 : 0);
-    static constexpr uint32_t kOffDesc = kOffCol + (kQInSmem ? kQ8Warps * kRows * 8 : 0);
-    static constexpr uint32_t kOffBar = kOffDesc + kQ8Warps * 16;
-    static constexpr uint32_t kOffP = kOffBar + kQ8Warps * kStages * 8;
+    static constexpr uint32_t kOffFirst = kWarps * kRing;
+    static constexpr uint32_t kOffLastMl = kOffFirst + (kFirstInSmem ? kWarps * piece_floats(kRows) * 4 : 0);
+    static constexpr uint32_t kOffQ = kOffLastMl + kWarps * kRows * 8;
+    static constexpr uint32_t kOffCol = kOffQ + (kQInSmem ? kWarps * NT * 16 * 32 * 4 : 0);
+    static constexpr uint32_t kOffDesc = kOffCol + (kQInSmem ? kWarps * kRows * 8 : 0);
+    static constexpr uint32_t kOffBar = kOffDesc + kWarps * 16;
+    static constexpr uint32_t kOffP = kOffBar + kWarps * kStages * 8;
     static constexpr uint32_t kOffLen = kOffP + (kQ8MaxSeqs + 4) * 4;
     static constexpr uint32_t kOffRow0 = kOffLen + kQ8MaxSeqs * 4;   // several tokens: first row and count
     static constexpr uint32_t kOffN = kOffRow0 + kQ8MaxSeqs * 4;
@@ -156,10 +158,10 @@ __device__ __forceinline__ size_t row_at(const Q8Launch& p, int row0, int h, int
 // a fragment (four row pairs at once) then meet no bank conflict.
 __device__ __forceinline__ int chunk_of(int r, int c) { return r * (kHeadDim / 4) + (c ^ (r >> 1 & 3)); }
 
-template <typename T, int NT, bool kMulti>
-__global__ void __launch_bounds__(kQ8Threads, 1)
+template <typename T, int NT, int kW, bool kMulti>
+__global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
     q8_attend_kernel(const Q8Launch p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-    using M = Q8Smem<NT>;
+    using M = Q8Smem<NT, kW>;
     constexpr int kStages = M::kStages, kStartUnits = start_units(NT * 8);
     constexpr uint32_t kAll = 0xffffffffu;
     const DecodeQ8Args& a = p.a;
@@ -189,9 +191,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     // ---- lengths, and the units of one kv head before each sequence (P) ----
     const int S = a.num_seqs, Hkv = a.num_kv_heads, group = p.group;
     {
-        __shared__ int warp_sum_of[kQ8Warps];
+        __shared__ int warp_sum_of[M::kWarps];
         int carry = 0;
-        for (int s0 = 0; s0 < S; s0 += kQ8Threads) {
+        for (int s0 = 0; s0 < S; s0 += M::kThreads) {
             const int s = s0 + tid;
             int w = 0;
             if (s < S) {
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             __syncthreads();
             int before = carry + incl - w;
 #pragma unroll
-            for (int i = 0; i < kQ8Warps; ++i) {
+            for (int i = 0; i < M::kWarps; ++i) {
                 const int x = warp_sum_of[i];
                 if (i < warp) before += x;
                 carry += x;
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
 
     const long long total = (long long)P[S] * Hkv;
     // share i of the line begins at unit floor(total * i / shares) (32-bit divisions: 64-bit ones take 0.3 us each)
-    const unsigned shares = gridDim.x * kQ8Warps, me = blockIdx.x * kQ8Warps + warp;
+    const unsigned shares = gridDim.x * M::kWarps, me = blockIdx.x * M::kWarps + warp;
     const long long each = total >> 32 ? total / shares : (long long)((unsigned)total / shares);
     const unsigned odd = (unsigned)(total - each * shares);
     auto share_at = [&](unsigned i) { return each * i + (odd * i) / shares; };
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     auto first_of = [&](int w) {
         return reinterpret_cast<float4*>(
             M::kFirstInSmem ? reinterpret_cast<float*>(smem + M::kOffFirst) + w * piece_floats(M::kRows)
-                            : p.firsts + ((size_t)blockIdx.x * kQ8Warps + w) * piece_floats(p.rows));
+                            : p.firsts + ((size_t)blockIdx.x * M::kWarps + w) * piece_floats(p.rows));
     };
     auto last_of = [&](int w) { return reinterpret_cast<float4*>(smem + w * M::kRing); };
     auto first_ml_of = [&](int w) { return reinterpret_cast<float2*>(first_of(w) + slot_rows * kHeadDim / 4); };
@@ -725,63 +727,64 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     // ends there, every other warp its last.  The rows of all chains are dealt to the warps, four at a time.
     int left_first = 3, left_last = 0, left_seg = 0;
     {
-        const WarpPieces x = wp[lane % kQ8Warps];
-        const unsigned low = (1u << kQ8Warps) - 1;
+        constexpr int kGroup = M::kWarps <= 8 ? 8 : 16, kTake = 32 / kGroup;   // lanes a row, rows at a time
+        const WarpPieces x = lane < M::kWarps ? wp[lane] : WarpPieces{kNoUnits, 0, 0, 0};
+        const unsigned low = (1u << M::kWarps) - 1;
         const unsigned some = ~__ballot_sync(kAll, x.flags & kNoUnits) & low;
         const unsigned firsts = __ballot_sync(kAll, x.flags & kHasFirst) & low;
         const unsigned lasts = __ballot_sync(kAll, x.flags & kHasLast) & low;
         const unsigned opens = lasts & ~__ballot_sync(kAll, x.flags & kThrough);
         const int last_warp = some ? 31 - __clz(some) : 0;
-        // events: a first piece at its warp, and at kQ8Warps the chain still open at the end
-        unsigned events = firsts | ((lasts >> last_warp & 1) << kQ8Warps);
+        // events: a first piece at its warp, and at M::kWarps the chain still open at the end
+        unsigned events = firsts | ((lasts >> last_warp & 1) << M::kWarps);
         if (some) left_first = 0;
         if (events) {
             const int e = __ffs(events) - 1;
-            if (!(opens & ((1u << e) - 1))) left_first = e < kQ8Warps ? 1 : 2;
+            if (!(opens & ((1u << e) - 1))) left_first = e < M::kWarps ? 1 : 2;
         }
-        if ((events >> kQ8Warps) && (opens >> (firsts ? 31 - __clz(firsts) : 0))) {
+        if ((events >> M::kWarps) && (opens >> (firsts ? 31 - __clz(firsts) : 0))) {
             left_last = 1;
             left_seg = __shfl_sync(kAll, x.last_seg, last_warp);
         }
-        const int batches = (p.rows + 3) / 4, items = __popc(events) * batches;
-        for (int item = warp; item < items; item += kQ8Warps) {
+        const int batches = (p.rows + kTake - 1) / kTake, items = __popc(events) * batches;
+        for (int item = warp; item < items; item += M::kWarps) {
             unsigned ev = events;
             int k = item;
             for (; k >= batches; k -= batches) ev &= ev - 1;
             const int we = __ffs(ev) - 1;
             const unsigned below = events & ((1u << we) - 1);
-            const bool closed = we < kQ8Warps;
+            const bool closed = we < M::kWarps;
             const unsigned opener = opens & ((1u << we) - 1) & ~((1u << (below ? 31 - __clz(below) : 0)) - 1);
             const bool before = opener == 0;
             const int ws = before ? 0 : __ffs(opener) - 1;
             const unsigned pieces = some & ~((1u << ws) - 1) & ((2u << we) - 1);
             const int seg = __shfl_sync(kAll, closed ? x.first_seg : x.last_seg, closed ? we : last_warp);
-            const int sg = seg >> 16, hh = seg & 0xffff, r0 = k * 4;
+            const int sg = seg >> 16, hh = seg & 0xffff, r0 = k * kTake;
             const int first = kMulti ? row0_of[sg] : sg, rows = (kMulti ? n_of[sg] : 1) * group;
             if (r0 >= rows) continue;
             float* to = p.parts + ((size_t)blockIdx.x * 2 + (before ? 0 : 1)) * piece_floats(p.rows);
             // four rows at a time: lane 8 i + w weighs warp w's piece of row i, then every lane has four
             // elements of each row
-            const int w = lane % kQ8Warps, rw = r0 + lane / kQ8Warps;
+            const int w = lane % kGroup, rw = r0 + lane / kGroup;
             float2 ml = make_float2(-INFINITY, 0.f);
             if ((pieces >> w & 1) && rw < rows) ml = (closed && w == we ? first_ml_of(w) : last_ml_of(w))[rw];
             float m = ml.x;
 #pragma unroll
-            for (int k = 1; k < kQ8Warps; k <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
+            for (int k = 1; k < kGroup; k <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
             const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
             float l = f * ml.y;
 #pragma unroll
-            for (int k = 1; k < kQ8Warps; k <<= 1) l += __shfl_xor_sync(kAll, l, k);
-            float4 acc[4];
+            for (int k = 1; k < kGroup; k <<= 1) l += __shfl_xor_sync(kAll, l, k);
+            float4 acc[kTake];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < kTake; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
             for (unsigned todo = pieces; todo; todo &= todo - 1) {
                 const int pw = __ffs(todo) - 1;
                 const float4* slot = closed && pw == we ? first_of(pw) : last_of(pw);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float fw = __shfl_sync(kAll, f, i * kQ8Warps + pw);
+                for (int i = 0; i < kTake; ++i) {
+                    const float fw = __shfl_sync(kAll, f, i * kGroup + pw);
                     if (r0 + i < rows) {
                         const float4 v = slot[chunk_of(r0 + i, lane)];
                         acc[i].x = fmaf(fw, v.x, acc[i].x);
@@ -792,8 +795,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float mi = __shfl_sync(kAll, m, i * kQ8Warps), li = __shfl_sync(kAll, l, i * kQ8Warps);
+            for (int i = 0; i < kTake; ++i) {
+                const float mi = __shfl_sync(kAll, m, i * kGroup), li = __shfl_sync(kAll, l, i * kGroup);
                 const int r = r0 + i;
                 if (r < rows) {
                     if (closed && !before) {
@@ -815,7 +818,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             int i = max(0, min((int)((float)last_unit * (float)shares / (float)total), (int)shares - 1));
             while (share_at(i) > last_unit) --i;
             while (share_at(i + 1) <= last_unit) ++i;
-            left.end = i / kQ8Warps;
+            left.end = i / M::kWarps;
             left.row0 = kMulti ? row0_of[sg] : sg;
             left.rows = (kMulti ? n_of[sg] : 1) * group;
             left.head = hh;
@@ -825,7 +828,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     if (!kMulti) {   // rows of empty sequences
         for (int e = blockIdx.x; e < S; e += gridDim.x)
             if (lens[e] == 0)
-                for (int i = tid; i < a.num_q_heads * kHeadDim / 8; i += kQ8Threads)
+                for (int i = tid; i < a.num_q_heads * kHeadDim / 8; i += M::kThreads)
                     reinterpret_cast<uint4*>(a.out)[(size_t)e * a.num_q_heads * kHeadDim / 8 + i] = make_uint4(0, 0, 0, 0);
     }
 }
@@ -901,24 +904,30 @@ long long line_bound(int num_seqs, int num_kv_heads, int block_size, int max_blo
     return slice_of(num_seqs, block_size, max_blocks, rows) * num_kv_heads * units_bound(block_size, max_blocks, rows);
 }
 
+struct Q8Grid {
+    int ctas, warps;
+};
+
 // One CTA per SM, fewer for little work: a cut between CTAs costs the joining launch (2.5 us), so at the longest
 // contexts the tables allow one CTA takes up to eight units a warp alone, and several take four at least.
-int q8_ctas(int num_seqs, int num_kv_heads, int block_size, int max_blocks, int rows) {
+Q8Grid q8_grid(int num_seqs, int num_kv_heads, int block_size, int max_blocks, int rows) {
     const long long units = line_bound(num_seqs, num_kv_heads, block_size, max_blocks, rows);
-    if (units <= 8 * kQ8Warps) return 1;
-    return (int)min((units + 4 * kQ8Warps - 1) / (4 * kQ8Warps), (long long)sm_count_current());
+    const int sms = sm_count_current();
+    const int warps = rows <= 8 && (long long)num_seqs * num_kv_heads >= 2LL * kFewWarps * sms ? kManyWarps : kFewWarps;
+    if (units <= 8 * warps) return Q8Grid{1, warps};
+    return Q8Grid{(int)min((units + 4 * warps - 1) / (4 * warps), (long long)sms), warps};
 }
 
 struct Q8Layout {
     size_t firsts, pieces, bytes;
 };
 
-Q8Layout q8_layout(int ctas, int rows) {
+Q8Layout q8_layout(const Q8Grid& grid, int rows) {
     Q8Layout w;
     const size_t piece = (size_t)piece_floats(rows) * sizeof(float);
-    w.firsts = align256(2 * ctas * piece);
-    w.pieces = w.firsts + (rows > 16 ? align256((size_t)ctas * kQ8Warps * piece) : 0);
-    w.bytes = w.pieces + align256(ctas * sizeof(CtaPieces));
+    w.firsts = align256(2 * (size_t)grid.ctas * piece);
+    w.pieces = w.firsts + (rows > 16 ? align256((size_t)grid.ctas * grid.warps * piece) : 0);
+    w.bytes = w.pieces + align256((size_t)grid.ctas * sizeof(CtaPieces));
     return w;
 }
 
@@ -934,10 +943,10 @@ bool encode_q8_map(const void* base, unsigned long long rows, CUtensorMap* out) 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int NT, bool kMulti>
+template <typename T, int NT, int kW, bool kMulti>
 cudaError_t launch_nt(const Q8Launch& p, int ctas, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
-    constexpr size_t smem = 1024 + Q8Smem<NT>::kBytes;
-    auto kernel = q8_attend_kernel<T, NT, kMulti>;
+    constexpr size_t smem = 1024 + Q8Smem<NT, kW>::kBytes;
+    auto kernel = q8_attend_kernel<T, NT, kW, kMulti>;
     cudaError_t e;
     static std::atomic<unsigned long long> allowed{0};   // devices on which the kernel may have its shared memory
     int dev = 0;
@@ -948,7 +957,7 @@ cudaError_t launch_nt(const Q8Launch& p, int ctas, const CUtensorMap& k, const C
         if (e != cudaSuccess) return e;
         allowed.fetch_or(dev > 63 ? 0 : bit);
     }
-    e = launch_pdl(kernel, dim3(ctas), dim3(kQ8Threads), smem, stream, p, k, v);
+    e = launch_pdl(kernel, dim3(ctas), dim3(Q8Smem<NT, kW>::kThreads), smem, stream, p, k, v);
     if (e != cudaSuccess || ctas == 1) return e;
     // as many warps to a row as a segment has pieces when all are equally long
     const int pieces = ctas / max(1, min(ctas, p.a.num_seqs * p.a.num_kv_heads));
@@ -958,12 +967,15 @@ cudaError_t launch_nt(const Q8Launch& p, int ctas, const CUtensorMap& k, const C
 }
 
 template <typename T, bool kMulti>
-cudaError_t launch_rows(const Q8Launch& p, int ctas, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t stream) {
+cudaError_t launch_rows(const Q8Launch& p, const Q8Grid& grid, const CUtensorMap& k, const CUtensorMap& v,
+                        cudaStream_t stream) {
+    const int ctas = grid.ctas;
+    if (grid.warps == kManyWarps) return launch_nt<T, 1, kManyWarps, kMulti>(p, ctas, k, v, stream);
     switch ((p.rows + 7) / 8) {
-        case 1: return launch_nt<T, 1, kMulti>(p, ctas, k, v, stream);
-        case 2: return launch_nt<T, 2, kMulti>(p, ctas, k, v, stream);
-        case 3: return launch_nt<T, 3, kMulti>(p, ctas, k, v, stream);
-        default: return launch_nt<T, 4, kMulti>(p, ctas, k, v, stream);
+        case 1: return launch_nt<T, 1, kFewWarps, kMulti>(p, ctas, k, v, stream);
+        case 2: return launch_nt<T, 2, kFewWarps, kMulti>(p, ctas, k, v, stream);
+        case 3: return launch_nt<T, 3, kFewWarps, kMulti>(p, ctas, k, v, stream);
+        default: return launch_nt<T, 4, kFewWarps, kMulti>(p, ctas, k, v, stream);
     }
 }
 
@@ -973,13 +985,14 @@ size_t q8_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int m
                           int max_blocks_per_seq) {
     if (num_seqs == 0) return 0;
     const int rows = num_q_heads / num_kv_heads * max_q;
-    const int ctas = q8_ctas(num_seqs, num_kv_heads, block_size, max_blocks_per_seq, rows);
-    return ctas == 1 && rows <= 16 ? 0 : q8_layout(ctas, rows).bytes;
+    const Q8Grid grid = q8_grid(num_seqs, num_kv_heads, block_size, max_blocks_per_seq, rows);
+    return grid.ctas == 1 && rows <= 16 ? 0 : q8_layout(grid, rows).bytes;
 }
 
 bool q8_line_fits(int num_seqs, int num_kv_heads, int block_size, int max_blocks_per_seq) {
-    const int ctas = q8_ctas(num_seqs, num_kv_heads, block_size, max_blocks_per_seq, kQ8MaxRows);
-    return line_bound(num_seqs, num_kv_heads, block_size, max_blocks_per_seq, kQ8MaxRows) / (ctas * kQ8Warps) < (1LL << 30);
+    const Q8Grid grid = q8_grid(num_seqs, num_kv_heads, block_size, max_blocks_per_seq, kQ8MaxRows);
+    return line_bound(num_seqs, num_kv_heads, block_size, max_blocks_per_seq, kQ8MaxRows) / (grid.ctas * kFewWarps) <
+           (1LL << 30);
 }
 
 cudaError_t launch_decode_q8(const DecodeQ8Args& a, int dtype, void* workspace, cudaStream_t stream) {
@@ -997,8 +1010,8 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, int dtype, void* workspace, 
     p.group = a.num_q_heads / a.num_kv_heads;
     p.group_inv = (65536u + p.group - 1) / p.group;
     p.rows = p.group * a.max_q;
-    const int ctas = q8_ctas(a.num_seqs, a.num_kv_heads, a.block_size, a.max_blocks_per_seq, p.rows);
-    const Q8Layout w = q8_layout(ctas, p.rows);
+    const Q8Grid grid = q8_grid(a.num_seqs, a.num_kv_heads, a.block_size, a.max_blocks_per_seq, p.rows);
+    const Q8Layout w = q8_layout(grid, p.rows);
     char* ws = static_cast<char*>(workspace);
     p.parts = reinterpret_cast<float*>(ws);
     p.firsts = reinterpret_cast<float*>(ws + w.firsts);
@@ -1019,11 +1032,11 @@ cudaError_t launch_decode_q8(const DecodeQ8Args& a, int dtype, void* workspace, 
         }
         cudaError_t e;
         if (dtype == PA_BF16)
-            e = a.q_start ? launch_rows<__nv_bfloat16, true>(p, ctas, k, v, stream)
-                          : launch_rows<__nv_bfloat16, false>(p, ctas, k, v, stream);
+            e = a.q_start ? launch_rows<__nv_bfloat16, true>(p, grid, k, v, stream)
+                          : launch_rows<__nv_bfloat16, false>(p, grid, k, v, stream);
         else
-            e = a.q_start ? launch_rows<__half, true>(p, ctas, k, v, stream)
-                          : launch_rows<__half, false>(p, ctas, k, v, stream);
+            e = a.q_start ? launch_rows<__half, true>(p, grid, k, v, stream)
+                          : launch_rows<__half, false>(p, grid, k, v, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -220,6 +220,17 @@ def test_several_tokens_of_many_sequences():
     Problem(lens.tolist(), 2, 1, 16, torch.float16, new=new.tolist(), seed=98).run()
 
 
+@pytest.mark.parametrize("new", [False, True])
+def test_many_short_segments(new):
+    """More than two segments begin in every warp's share: the grid of twelve warps a CTA."""
+    rng = np.random.default_rng(100)
+    lens = rng.integers(0, 70, 640)
+    lens[100] = 5000                          # and one that is cut many times
+    n = np.minimum(lens, rng.integers(0, 3, 640)).tolist() if new else None
+    assert 640 * 4 >= 2 * 8 * 152
+    Problem(lens.tolist(), 12, 4, 16, torch.float16, new=n, seed=100).run()
+
+
 def test_no_sequences_and_no_rows():
     p = Problem([20, 33], 4, 1, 16, torch.float16, new=[0, 0], seed=99)
     p.upload()
