@@ -22,7 +22,8 @@ namespace {
 constexpr int kRopeThreads = 256;   // 128 where one vector per thread is enough
 constexpr int kRopeBatch = 2;       // vectors (pairs of vectors) of a thread in flight
 constexpr int kRopePerSm = 5;       // CTAs (of 256 threads, 51 registers) per SM
-constexpr int kRopeTokens = 16;     // tokens of a CTA at most
+constexpr int kRopeTokens = 16;     // tokens of a CTA at most; their cosines and sines fit in 48 KB
+constexpr int kRopePairs = 48 * 1024 / (int)sizeof(float2);
 
 __device__ __forceinline__ uint64_t turns64(double f) {
     const double t = f * 0.15915494309189533577;   // 1 / (2 pi)
@@ -165,7 +166,8 @@ template <typename T>
 static cudaError_t launch_type(const RopeArgs& a, cudaStream_t stream) {
     const int rot = a.rotary_dim / 8, per_head = (a.interleaved ? rot : rot / 2) + a.head_dim / 8 - rot;
     // whole waves of CTAs, each CTA with at most kRopeTokens tokens
-    const long long slots = kRopePerSm * sm_count_current(), most = slots * kRopeTokens;
+    const long long slots = kRopePerSm * sm_count_current();
+    const long long most = slots * min(kRopeTokens, kRopePairs / (a.rotary_dim / 2));
     const long long waves = (a.num_tokens + most - 1) / most;
     const int tokens = (int)((a.num_tokens + slots * waves - 1) / (slots * waves));
     const bool small = tokens * (a.num_q_heads + a.num_kv_heads) * per_head <= 128;

@@ -164,6 +164,18 @@ def test_rope_beyond_32_bit_offsets():
     assert not x[:-3].any()
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_of_the_widest_head_and_many_tokens(interleaved):
+    """Several tokens of a CTA, whose cosines and sines fill what shared memory it may have."""
+    q, k, pos = _inputs(12500, 1, 1, 1024, torch.bfloat16, seed=21)
+    f, m = pa.rope_frequencies(1024)
+    oq, ok = pa.rope(q, k, pos.to(DEV), f, interleaved=interleaved)
+    torch.cuda.synchronize()
+    for at in (slice(0, 40), slice(6230, 6270), slice(12460, 12500)):
+        _check(oq[at], q[at], pos[at], f, m, interleaved)
+        _check(ok[at], k[at], pos[at], f, m, interleaved)
+
+
 def test_rope_refuses():
     q, k, pos = _inputs(4, 2, 1, 128, torch.float16, seed=17)
     p = pos.to(DEV)
