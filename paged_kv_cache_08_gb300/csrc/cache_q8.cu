@@ -17,7 +17,11 @@
 // decode step's form, has a kernel of its own.
 //
 // read_q8: code * 2^e rounded to the pool's 16-bit type (bf16 exactly), beyond its range to its
-// largest value; one thread per 16 codes of K and of V.  Both are bound by HBM.
+// largest value; one thread per 16 codes of K and of V.
+//
+// Both are bound by HBM: 512 rows x 16 sequences x 32 heads appended in 34 us (32-token blocks; 0.87 of a copy's
+// rate), 2048 blocks of 32 rows x 32 heads read back in 241 us (0.98).  One row a sequence (64 x 2 heads) takes
+// 2.2 us: the launch, and length, table and exponent one after another.
 #include <type_traits>
 
 #include "q8.cuh"
