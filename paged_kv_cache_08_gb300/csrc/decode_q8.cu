@@ -245,8 +245,52 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
     const long long each = total >> 32 ? total / shares : (long long)((unsigned)total / shares);
     const unsigned odd = (unsigned)(total - each * shares);
     auto share_at = [&](unsigned i) { return each * i + (odd * i) / shares; };
-    const long long u0 = share_at(me), u1 = share_at(me + 1);
-    const int units = (int)(u1 - u0);
+    // A cut among a segment's start units goes before them: its first tile begins the segment in any case, and the
+    // share before would leave an empty piece.  In a short segment a cut next to its first or last tile goes to the
+    // begin or the end, too, since the piece costs more than the tile (four contexts of up to 64 tokens 7.5 us without,
+    // 6.2 with; 64 contexts of up to 2048 tokens, 30 rows 25.9 and 25.4; few rows of longer contexts gain nothing:
+    // their shares only become unequal).
+    auto near_of = [&](int w) {
+        return (M::kWarps > kFewWarps || NT > 1 || gridDim.x == 1) && w <= kStartUnits + 8 ? 1 : 0;
+    };
+    // The share's first unit (r of segment (s, h)) and, by the upper half of the warp, the next share's.
+    int s, h, r, units;
+    long long u0;
+    {
+        const int half = lane & 16, of_half = lane & 15;
+        long long u = share_at(me + (half >> 4));
+        s = 0;   // the last s with P[s] * Hkv <= u
+        for (int n = S; n > 1;) {
+            n = (n + 15) / 16;
+            const int at = s + of_half * n;
+            const unsigned m = __ballot_sync(kAll, at < S && (long long)P[min(at, S)] * Hkv <= u) >> half & 0xffff;
+            s += (31 - __clz(m)) * n;
+        }
+        const int w = max(1, P[s + 1] - P[s]);
+        const unsigned long long rem = u - (long long)P[s] * Hkv;
+        h = rem <= 0xffffffffu ? (uint32_t)rem / w : (int)(rem / w);
+        r = (int)(rem - (unsigned long long)h * w);
+        if (u < total) {
+            const int near = near_of(w);
+            if (r <= kStartUnits + near) {
+                u -= r;
+                r = 0;
+            } else if (w - r <= near) {
+                u += w - r;
+                r = 0;
+                if (++h == Hkv) {
+                    h = 0;
+                    do ++s;
+                    while (s < S && P[s + 1] == P[s]);
+                }
+            }
+        }
+        u0 = __shfl_sync(kAll, u, 0);
+        units = (int)(__shfl_sync(kAll, u, 16) - u0);
+        s = __shfl_sync(kAll, s, 0);
+        h = __shfl_sync(kAll, h, 0);
+        r = __shfl_sync(kAll, r, 0);
+    }
 
     // ---- per-lane fragment addresses inside a tile (128-byte swizzle: 16-byte unit ^ (row & 7)) ----
     const uint32_t k_off0 = g * 128 + ((uint32_t)((2 * t) ^ g) << 4);
@@ -271,7 +315,7 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
     uint32_t qreg[M::kQInSmem ? 1 : NT][16];
     uint4* qsm = reinterpret_cast<uint4*>(smem + M::kOffQ) + warp * NT * 4 * 32 + lane;
     uint4 qn[M::kQInSmem ? 1 : NT][4];   // Q rows of the segment that comes next, as they lie in memory
-    int s = 0, h = 0, L = 0, row0 = 0, nrows = 0, p0 = 0;
+    int L = 0, row0 = 0, nrows = 0, p0 = 0;
     uint32_t phases = 0;
 
     // Loads of Q row 8 nt + g, dims 32 t .. 32 t + 31 of segment (s, h).
@@ -593,12 +637,6 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
     // ---- the stream ----
     WarpPieces mine{units == 0 ? kNoUnits : 0, 0, 0, 0};
     if (units > 0) {
-        {   // the last s with P[s] * Hkv <= u0
-            unsigned m = __ballot_sync(kAll, lane * 32 < S && (long long)P[min(lane * 32, S)] * Hkv <= u0);
-            s = (31 - __clz(m)) * 32;
-            m = __ballot_sync(kAll, s + lane < S && (long long)P[min(s + lane, S)] * Hkv <= u0);
-            s += 31 - __clz(m);
-        }
         // of the unit this lane owns in a window of 32: the pool row of its tile's first token (-1: a start
         // unit or none, -2: a block outside the pool) and its block's exponents
         int A_y = -1, A_ke = 0, A_ve = 0, B_y = -1, B_ke = 0, B_ve = 0, lane_s = s;
@@ -624,13 +662,6 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
             ke = __ldg(a.k_exp + tile);
             ve = __ldg(a.v_exp + tile);
         };
-        int r;   // unit of the segment at the head of the share
-        {
-            const uint32_t w = P[s + 1] - P[s];
-            const unsigned long long rem = u0 - (long long)P[s] * Hkv;
-            h = rem <= 0xffffffffu ? (uint32_t)rem / w : (int)(rem / w);
-            r = (int)(rem - (unsigned long long)h * w);
-        }
         fetch_q(s, h);
         look(lane, A_y, A_ke, A_ve);
         auto issue = [&](int j, int y) {   // by the lane that owns unit j
@@ -772,6 +803,10 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
             // four rows at a time: lane 8 i + w weighs warp w's piece of row i, then every lane has four
             // elements of each row
             const int w = lane % kGroup, rw = r0 + lane / kGroup;
+            float4 vf[kTake];   // the piece that ends the chain (in memory with many rows), on its way early
+#pragma unroll
+            for (int i = 0; i < kTake; ++i)
+                if (closed && r0 + i < rows) vf[i] = first_of(we)[chunk_of(r0 + i, lane)];
             float2 ml = make_float2(-INFINITY, 0.f);
             if ((pieces >> w & 1) && rw < rows) ml = (closed && w == we ? first_ml_of(w) : last_ml_of(w))[rw];
             float m = ml.x;
@@ -784,22 +819,42 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
             float4 acc[kTake];
 #pragma unroll
             for (int i = 0; i < kTake; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int last_end = closed ? we : last_warp + 1;
 #pragma unroll 1
-            for (unsigned todo = pieces; todo; todo &= todo - 1) {
-                const int pw = __ffs(todo) - 1;
-                const float4* slot = closed && pw == we ? first_of(pw) : last_of(pw);
+            for (int pw = ws; pw < last_end; pw += 2) {   // last pieces, two at a time
+                const bool one = pieces >> pw & 1, two = pw + 1 < last_end && (pieces >> (pw + 1) & 1);
+                float4 v[2][kTake];
 #pragma unroll
                 for (int i = 0; i < kTake; ++i) {
-                    const float fw = __shfl_sync(kAll, f, i * kGroup + pw);
+                    v[0][i] = v[1][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (one && r0 + i < rows) v[0][i] = last_of(pw)[chunk_of(r0 + i, lane)];
+                    if (two && r0 + i < rows) v[1][i] = last_of(pw + 1)[chunk_of(r0 + i, lane)];
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < kTake; ++i) {
+                        const float fw = __shfl_sync(kAll, f, i * kGroup + ((pw + k) & (kGroup - 1)));
+                        const float4 x = v[k][i];
+                        if (k ? two : one) {
+                            acc[i].x = fmaf(fw, x.x, acc[i].x);
+                            acc[i].y = fmaf(fw, x.y, acc[i].y);
+                            acc[i].z = fmaf(fw, x.z, acc[i].z);
+                            acc[i].w = fmaf(fw, x.w, acc[i].w);
+                        }
+                    }
+            }
+            if (closed)
+#pragma unroll
+                for (int i = 0; i < kTake; ++i) {
+                    const float fw = __shfl_sync(kAll, f, i * kGroup + we);
                     if (r0 + i < rows) {
-                        const float4 v = slot[chunk_of(r0 + i, lane)];
-                        acc[i].x = fmaf(fw, v.x, acc[i].x);
-                        acc[i].y = fmaf(fw, v.y, acc[i].y);
-                        acc[i].z = fmaf(fw, v.z, acc[i].z);
-                        acc[i].w = fmaf(fw, v.w, acc[i].w);
+                        acc[i].x = fmaf(fw, vf[i].x, acc[i].x);
+                        acc[i].y = fmaf(fw, vf[i].y, acc[i].y);
+                        acc[i].z = fmaf(fw, vf[i].z, acc[i].z);
+                        acc[i].w = fmaf(fw, vf[i].w, acc[i].w);
                     }
                 }
-            }
 #pragma unroll
             for (int i = 0; i < kTake; ++i) {
                 const float mi = __shfl_sync(kAll, m, i * kGroup), li = __shfl_sync(kAll, l, i * kGroup);
@@ -820,10 +875,13 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
         if (left_last) {
             const int sg = left_seg >> 16, hh = left_seg & 0xffff;
             // the share that holds its last unit: a guess good to a share or two, put right
-            const long long last_unit = (long long)P[sg] * Hkv + (long long)(hh + 1) * (P[sg + 1] - P[sg]) - 1;
+            const int w = P[sg + 1] - P[sg];
+            const long long last_unit = (long long)P[sg] * Hkv + (long long)(hh + 1) * w - 1;
             int i = max(0, min((int)((float)last_unit * (float)shares / (float)total), (int)shares - 1));
             while (share_at(i) > last_unit) --i;
             while (share_at(i + 1) <= last_unit) ++i;
+            const int near = near_of(w);   // (cuts moved to the segment's end)
+            while (last_unit + 1 - share_at(i) <= near && w - (last_unit + 1 - share_at(i)) > kStartUnits + near) --i;
             left.end = i / M::kWarps;
             left.row0 = kMulti ? row0_of[sg] : sg;
             left.rows = (kMulti ? n_of[sg] : 1) * group;
