@@ -76,6 +76,22 @@ __device__ __forceinline__ uint2 rescale8(uint2 codes, float down) {
     return make_uint2(n[0], n[1]);
 }
 
+// The rows r, r + step, .. below `end` (8 codes of each, rows kHeadDim apart from `dst` on) under a grown exponent,
+// eight loads in flight (128 ragged sequences of 128-token blocks whose exponents all grow: 14 us beyond the fill that
+// lowers them, 25 one row after another; 64 decode steps of 16-token blocks 4.2 and 6.8).
+__device__ __forceinline__ void rescale_rows(uint8_t* dst, int r, int end, int step, float down) {
+    constexpr int kBatch = 8;
+    for (; r < end; r += kBatch * step) {
+        uint2 c[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (r + i * step < end) c[i] = *reinterpret_cast<const uint2*>(dst + (r + i * step) * kHeadDim);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (r + i * step < end) *reinterpret_cast<uint2*>(dst + (r + i * step) * kHeadDim) = rescale8(c[i], down);
+    }
+}
+
 // One new row per sequence (query_start == null): a warp takes eight kv heads of a sequence, its lower half
 // their K rows and its upper half their V rows, so that the walk from length to table to exponent is made once.
 constexpr int kOneHeads = 8;
@@ -127,13 +143,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_one_q8_kernel(const 
         const int e = lo == 0 ? need : max(e_old[i], need);
         uint8_t* dst = (is_v ? a.v_cache : a.k_cache) + (tile0 + i) * B * kHeadDim + c * 8;
         *reinterpret_cast<uint2*>(dst + lo * kHeadDim) = quantise8<T>(x[i], exp2_int(-e));
-        if (e > e_old[i] && lo > 0) {   // earlier rows: the same values under the grown exponent
-            const float down = exp2_int(e_old[i] - e);
-            for (int r = 0; r < lo; ++r) {
-                uint2* row = reinterpret_cast<uint2*>(dst + r * kHeadDim);
-                *row = rescale8(*row, down);
-            }
-        }
+        if (e > e_old[i] && lo > 0) rescale_rows(dst, 0, lo, 1, exp2_int(e_old[i] - e));   // earlier rows
         if (c == 0) exps[i] = (int8_t)e;
     }
 }
@@ -243,14 +253,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kCtas) append_q8_kernel(con
         b -= stride_rows;
         load(b);
     }
-    if (e > e_old && lo > 0) {
-        // earlier rows: the same values under the grown exponent
-        const float down = exp2_int(e_old - e);
-        for (int r = part * 2 + lane / 16; r < lo; r += 2 * wpu) {
-            uint2* row = reinterpret_cast<uint2*>(dst + r * kHeadDim);
-            *row = rescale8(*row, down);
-        }
-    }
+    if (e > e_old && lo > 0) rescale_rows(dst, part * 2 + lane / 16, lo, 2 * wpu, exp2_int(e_old - e));   // earlier rows
     if (part == 0 && lane == 0) exps[tile] = (int8_t)e;
 }
 
