@@ -16,7 +16,8 @@
 // 2^-29 of the row's largest element).
 //
 // Work split: a segment is a (sequence, kv head); its 16-token tiles and two or three units for its start
-// and end (`start_units`) lie on a line, segment after segment, and every warp of the grid takes an equal, contiguous share of the line.
+// and end (`start_units`) lie on a line, segment after segment, and every warp of the grid takes an equal,
+// contiguous share of the line.
 // Warps are independent while they stream: each has a ring of tiles filled by its own TMA loads (2 KB of K
 // and of V, 128-byte swizzle, so that the 16-byte fragment loads below meet no bank conflict).  A segment
 // that lies in one warp's share goes straight to `out`; the pieces of a cut one meet in shared memory at the

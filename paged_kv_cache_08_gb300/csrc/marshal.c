@@ -231,8 +231,13 @@ static PyObject *attention(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
     } else {
         out = Py_NewRef(a[11]);
     }
-    void *o = want(out, dtype, dev, &ok);
-    if (ok) ok = sizes(out, no) == 3 && no[0] == nq[0] && no[1] == nq[1] && no[2] == nq[2];
+    void *o;
+    if (a[11] == Py_None) { /* like q, which is contiguous */
+        o = (void *)(uintptr_t)ask(out, s_data_ptr);
+    } else {
+        o = want(out, dtype, dev, &ok);
+        if (ok) ok = sizes(out, no) == 3 && no[0] == nq[0] && no[1] == nq[1] && no[2] == nq[2];
+    }
     void *w = ws ? (void *)(uintptr_t)ask(ws, s_data_ptr) : NULL;
     int rc = PA_ERR_INVALID_ARG;
     if (ok) {
@@ -350,16 +355,26 @@ static PyObject *rope(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
         PyErr_Clear();
         Py_RETURN_NONE;
     }
-    /* torch.empty_like keeps the strides of a dense tensor only: a slice's copy is contiguous */
+    /* torch.empty_like keeps the strides of a dense tensor only: a slice's copy is contiguous; that of tokens without
+     * gaps needs no look */
     PyObject *oq = a[6] == Py_None ? PyObject_CallOneArg(g_empty_like, a[0]) : Py_NewRef(a[6]);
     PyObject *ok_ = !oq ? NULL : !has_k ? Py_NewRef(Py_None) : a[7] == Py_None ? PyObject_CallOneArg(g_empty_like, a[1]) : Py_NewRef(a[7]);
     if (!oq || !ok_) {
         Py_XDECREF(oq);
         return NULL;
     }
-    void *to_q = want_rows(oq, dtype, dev, no, &oqs, &ok), *to_k = NULL;
-    for (int i = 0; ok && i < 3; ++i) ok = no[i] == nq[i];
-    if (has_k) {
+    void *to_q, *to_k = NULL;
+    if (a[6] == Py_None && qs == nq[1] * nq[2]) {
+        to_q = (void *)(uintptr_t)ask(oq, s_data_ptr);
+        oqs = qs;
+    } else {
+        to_q = want_rows(oq, dtype, dev, no, &oqs, &ok);
+        for (int i = 0; ok && i < 3; ++i) ok = no[i] == nq[i];
+    }
+    if (has_k && a[7] == Py_None && ks == nk[1] * nk[2]) {
+        to_k = (void *)(uintptr_t)ask(ok_, s_data_ptr);
+        oks = ks;
+    } else if (has_k) {
         to_k = want_rows(ok_, dtype, dev, no, &oks, &ok);
         for (int i = 0; ok && i < 3; ++i) ok = no[i] == nk[i];
     }
