@@ -231,6 +231,24 @@ def test_many_short_segments(new):
     Problem(lens.tolist(), 12, 4, 16, torch.float16, new=n, seed=100).run()
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_shares_cut_anywhere(seed):
+    """Random batches of short and long contexts under tables of random width: the warps' shares begin and end at every
+    place of a segment, and some are empty."""
+    rng = np.random.default_rng(900 + seed)
+    Hkv, group = int(rng.integers(1, 5)), int(rng.integers(1, 9))
+    S = int(rng.integers(1, 60))
+    top = int(rng.choice([40, 200, 1500]))
+    lens = rng.integers(0, top, S)
+    lens[rng.random(S) < 0.3] = rng.integers(0, 33)
+    new = None if seed % 3 == 0 else [int(min(x, n)) for x, n in zip(lens, rng.integers(0, 32 // group + 1, S))]
+    p = Problem([int(x) for x in lens], Hkv * group, Hkv, int(rng.choice([16, 32, 64, 128])),
+                [torch.float16, torch.bfloat16][seed % 2], new=new, seed=seed)
+    if seed % 4 == 1:
+        p.tables = np.concatenate([p.tables, np.full((S, 400), -1, dtype=np.int32)], 1)
+    p.run()
+
+
 def test_no_sequences_and_no_rows():
     p = Problem([20, 33], 4, 1, 16, torch.float16, new=[0, 0], seed=99)
     p.upload()
