@@ -42,6 +42,7 @@
 
 #include "decode_common.cuh"
 #include "q8.cuh"
+#include "q8_join.h"
 
 namespace pa {
 
@@ -104,11 +105,7 @@ struct Q8Smem {
     static_assert(1024 + kBytes + 64 <= 227 * 1024, "shared memory of one CTA");
 };
 
-// What a warp leaves for the end of its CTA (flags, then segments as s << 16 | h).
-constexpr int kHasFirst = 1;    // a piece of a segment begun before the warp's share, ended in it
-constexpr int kHasLast = 2;     // a piece of a segment that goes on
-constexpr int kThrough = 4;     // ... and that also began before the share
-constexpr int kNoUnits = 8;
+// What a warp leaves for the end of its CTA (flags as in q8_join.h, then segments as s << 16 | h).
 struct WarpPieces {
     int flags, first_seg, last_seg, pad;
 };
@@ -750,6 +747,7 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
             r = 0;
         }
         if (dead) {   // let the copies in flight land (again with a limit) before the CTA's memory is given up
+            mine.flags = kGaveUp;
             for (int j = i; j < min(units, i + kStages); ++j) {
                 const int yj = __shfl_sync(kAll, (j >> 5) == (i >> 5) ? A_y : B_y, j & 31);
                 if (yj >= 0) mbar_wait_bounded(&bars[j % kStages], (phases >> (j % kStages)) & 1);
@@ -760,41 +758,28 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
     __syncthreads();
 
     // ---- join the pieces of cut segments ----
-    // A first piece ends the chain of pieces that is open (or one from before this CTA), a last piece goes
-    // on with it (kThrough) or opens one.  Of a chain ws .. we, warp we gives its first piece if the chain
-    // ends there, every other warp its last.  The rows of all chains are dealt to the warps, four at a time.
-    int left_first = 3, left_last = 0, left_seg = 0;
+    // Of a chain of pieces (q8_join.h) ws .. we, warp we gives its first piece if the chain ends there, every other
+    // warp its last.  The rows of all chains are dealt to the warps, four at a time.
+    int left_first, left_last, left_seg = 0;
     {
         constexpr int kGroup = M::kWarps <= 8 ? 8 : 16, kTake = 32 / kGroup;   // lanes a row, rows at a time
         const WarpPieces x = lane < M::kWarps ? wp[lane] : WarpPieces{kNoUnits, 0, 0, 0};
-        const unsigned low = (1u << M::kWarps) - 1;
-        const unsigned some = ~__ballot_sync(kAll, x.flags & kNoUnits) & low;
-        const unsigned firsts = __ballot_sync(kAll, x.flags & kHasFirst) & low;
-        const unsigned lasts = __ballot_sync(kAll, x.flags & kHasLast) & low;
-        const unsigned opens = lasts & ~__ballot_sync(kAll, x.flags & kThrough);
-        const int last_warp = some ? 31 - __clz(some) : 0;
-        // events: a first piece at its warp, and at M::kWarps the chain still open at the end
-        unsigned events = firsts | ((lasts >> last_warp & 1) << M::kWarps);
-        if (some) left_first = 0;
-        if (events) {
-            const int e = __ffs(events) - 1;
-            if (!(opens & ((1u << e) - 1))) left_first = e < M::kWarps ? 1 : 2;
-        }
-        if ((events >> M::kWarps) && (opens >> (firsts ? 31 - __clz(firsts) : 0))) {
-            left_last = 1;
-            left_seg = __shfl_sync(kAll, x.last_seg, last_warp);
-        }
+        const CtaJoin join = cta_join(__ballot_sync(kAll, x.flags & kNoUnits), __ballot_sync(kAll, x.flags & kHasFirst),
+                                      __ballot_sync(kAll, x.flags & kHasLast), __ballot_sync(kAll, x.flags & kThrough),
+                                      __ballot_sync(kAll, x.flags & kGaveUp), M::kWarps);
+        const unsigned some = join.some, events = join.events;
+        const int last_warp = join.last_warp;
+        left_first = join.left_first;
+        left_last = join.left_last;
+        if (left_last) left_seg = __shfl_sync(kAll, x.last_seg, last_warp);
         const int batches = (p.rows + kTake - 1) / kTake, items = __popc(events) * batches;
         for (int item = warp; item < items; item += M::kWarps) {
             unsigned ev = events;
             int k = item;
             for (; k >= batches; k -= batches) ev &= ev - 1;
-            const int we = __ffs(ev) - 1;
-            const unsigned below = events & ((1u << we) - 1);
-            const bool closed = we < M::kWarps;
-            const unsigned opener = opens & ((1u << we) - 1) & ~((1u << (below ? 31 - __clz(below) : 0)) - 1);
-            const bool before = opener == 0;
-            const int ws = before ? 0 : __ffs(opener) - 1;
+            const JoinChain chain = join.chain(ev);
+            const int ws = chain.from, we = chain.to;
+            const bool closed = we < M::kWarps, before = chain.before;
             const unsigned pieces = some & ~((1u << ws) - 1) & ((2u << we) - 1);
             const int seg = __shfl_sync(kAll, closed ? x.first_seg : x.last_seg, closed ? we : last_warp);
             const int sg = seg >> 16, hh = seg & 0xffff, r0 = k * kTake;
