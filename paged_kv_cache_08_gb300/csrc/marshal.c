@@ -33,6 +33,20 @@ static long long ask(PyObject *t, PyObject *method) {
     return v;
 }
 
+/* The address of a tensor's data; 0 in *ok when it has none to give (a batched tensor inside torch.vmap is a plain
+ * torch.Tensor with a type, a device and a shape, but raises here). */
+static void *address(PyObject *t, int *ok) {
+    PyObject *r = PyObject_CallMethodNoArgs(t, s_data_ptr);
+    const unsigned long long v = r ? PyLong_AsUnsignedLongLong(r) : 0;
+    Py_XDECREF(r);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        *ok = 0;
+        return NULL;
+    }
+    return (void *)(uintptr_t)v;
+}
+
 static int is_dtype(PyObject *t, PyObject *dtype) {
     PyObject *d = PyObject_GetAttr(t, s_dtype);
     if (!d) {
@@ -50,7 +64,7 @@ static void *want(PyObject *t, PyObject *dtype, long long dev, int *ok) {
         *ok = 0;
         return NULL;
     }
-    return (void *)(uintptr_t)ask(t, s_data_ptr);
+    return address(t, ok);
 }
 
 /* Up to four sizes; the number of dimensions, or -1. */
@@ -97,7 +111,7 @@ static void *want_rows(PyObject *t, PyObject *dtype, long long dev, long long *n
         }
         if (n[0] > 1) *stride = a;
     }
-    return (void *)(uintptr_t)ask(t, s_data_ptr);
+    return address(t, ok);
 }
 
 /* The 16-bit type of `t` and its library number (-1: none), and its device if that is the current one. */
@@ -233,12 +247,12 @@ static PyObject *attention(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
     }
     void *o;
     if (a[11] == Py_None) { /* like q, which is contiguous */
-        o = (void *)(uintptr_t)ask(out, s_data_ptr);
+        o = address(out, &ok);
     } else {
         o = want(out, dtype, dev, &ok);
         if (ok) ok = sizes(out, no) == 3 && no[0] == nq[0] && no[1] == nq[1] && no[2] == nq[2];
     }
-    void *w = ws ? (void *)(uintptr_t)ask(ws, s_data_ptr) : NULL;
+    void *w = ws ? address(ws, &ok) : NULL;
     int rc = PA_ERR_INVALID_ARG;
     if (ok) {
         Py_BEGIN_ALLOW_THREADS;
@@ -365,14 +379,14 @@ static PyObject *rope(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
     }
     void *to_q, *to_k = NULL;
     if (a[6] == Py_None && qs == nq[1] * nq[2]) {
-        to_q = (void *)(uintptr_t)ask(oq, s_data_ptr);
+        to_q = address(oq, &ok);
         oqs = qs;
     } else {
         to_q = want_rows(oq, dtype, dev, no, &oqs, &ok);
         for (int i = 0; ok && i < 3; ++i) ok = no[i] == nq[i];
     }
     if (has_k && a[7] == Py_None && ks == nk[1] * nk[2]) {
-        to_k = (void *)(uintptr_t)ask(ok_, s_data_ptr);
+        to_k = address(ok_, &ok);
         oks = ks;
     } else if (has_k) {
         to_k = want_rows(ok_, dtype, dev, no, &oks, &ok);
