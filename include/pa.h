@@ -514,7 +514,8 @@ int pa_read_blocks_q8(const void* k_cache, const void* v_cache, const int8_t* k_
  * pa_decode_q8 / pa_multi_query_q8  [P4 §五.1; P1 address formula]
  * pa_decode and pa_multi_query over an 8-bit cache: the same rows, positions, clamping and outputs, with
  * K[t] and V[t] the values of the cached codes.  Products and sums in fp32, rounded once into `dtype`;
- * the softmax weights enter the PV product rounded to fp16 (11 bits).  pa_decode_q8: one query row per
+ * the softmax weights enter the PV product rounded to fp16: times their block's V scale, to 11 bits down to
+ * 2^-23 of the row's largest, below that to steps of 2^-33 of it.  pa_decode_q8: one query row per
  * sequence, L == 0 gives a zero row.  Rows of q and out that no sequence owns are neither read nor
  * written.  Tokens of a block whose table entry lies outside the pool are left out of the softmax and set
  * PA_DEV_BAD_BLOCK_ID (a row with no token left is zero).

@@ -10,9 +10,11 @@
 //   p_t = 2^(x_t - b),  P_t = p_t 2^ve,  O = sum P_t V_t (codes),  l = sum p_t,  out = O / l,
 // so V is never scaled, P_t stays in fp16's range whatever the blocks' scales (the base follows the maximum
 // of x_t + ve, not of the score), and b cancels.  p_t keeps the weights' sum: between blocks of scales 2^-60 and
-// 2^60 it spans 2^-68 .. 2^68 where it counts, inside fp32 (factors between bases may be subnormal: exp2f).
-// Codes become fp16 exactly; P is rounded to fp16 for the PV product (2^-11 of a weight, averaged over the
-// tokens; fp32 sums).  bf16 queries are scaled by a power of two per row into fp16's range (exact down to
+// 2^60 it spans 2^-51 .. 2^75 where it counts, inside fp32 (factors between bases may be subnormal: exp2f).
+// Codes become fp16 exactly; P is rounded to fp16 for the PV product (fp32 sums): 2^-11 of a weight, averaged
+// over the tokens.  The base leaves the largest P between 2^9 and 2^15, so that weights keep these bits down to
+// 2^-23 of the largest, and steps of 2^-33 of it below: a long context's tail beside one dominant token (a base
+// at the largest itself loses 3 % of the output with 131072 tokens and 98 % of the weight on one).  bf16 queries are scaled by a power of two per row into fp16's range (exact down to
 // 2^-29 of the row's largest element).
 //
 // Work split: a segment is a (sequence, kv head); its 16-token tiles and two or three units for its start
@@ -29,8 +31,8 @@
 //       product's k index is a permutation of the head's dims, the same one for the Q fragments.
 //   O += V^T P^T: the lane holds dims 16 g .. 16 g + 15 of tokens 2t, 2t+1, 2t+8, 2t+9; byte permutes pair
 //       the tokens of a dim.  P^T comes from S by movmatrix.
-// The base moves only when a score exceeds it by 2^8 (then O and l are rescaled), so most tiles need
-// no shuffle.
+// The base moves only when a weight grows to 2^6 of the largest when it was taken (then O and l are rescaled), so
+// most tiles need no shuffle.
 //
 // Bound by HBM (one byte per cached element) with up to 8 rows a segment: 16 contexts of 16384 tokens, 8 kv heads of
 // 4 rows 86 us (6.2 TB/s, 0.92 of a copy's rate), 256 short chats of 32 heads 58 us (5.2 TB/s).  With more rows by
@@ -58,7 +60,10 @@ constexpr uint32_t kTileBytes = 2 * kTileHalf;
 // What a segment's start and end cost, in tiles: with more than 16 rows Q is fetched as it begins, not ahead.
 __host__ __device__ constexpr int start_units(int rows) { return rows > 16 ? 3 : 2; }
 constexpr int kQ8MaxSeqs = 1024;                // sequences of one launch (their lengths stay on chip)
-constexpr float kBaseSlack = 8.f;               // log2: P stays below 2^8
+// log2 of P: a new base puts the largest at 2^kTopNew, and moves when one would exceed 2^kTopMost (fp16's largest is
+// below 2^16).  9 is the highest that costs nothing: one to five new tokens 22.8 us with 7 and 9, 23.5 with 11, 24.7
+// with 13, since the base then moves more often.
+constexpr float kTopNew = 9.f, kTopMost = 15.f;
 
 // Floats of a piece of `rows` rows: O, then (base, sum) of each row; a multiple of 16 bytes.
 __host__ __device__ constexpr int piece_floats(int rows) { return rows * kHeadDim + (2 * rows + 3) / 4 * 4; }
@@ -459,7 +464,7 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
         uint4 v2 = lds128(tile + v_off0 + 1024), v3 = lds128(tile + v_off1 + 1024);
 
         // x = score in log2 units; positions a row does not see to -inf
-        const float ks = exp2_int(ke), vs = exp2_int(ve), vef = (float)ve, slack = kBaseSlack - vef;
+        const float ks = exp2_int(ke), vs = exp2_int(ve), vef = (float)ve, slack = kTopMost - vef;
         const bool masked = t0 + kTile > p0 + 1;
         bool nan_v = false;
 #pragma unroll
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
                     float m = fmaxf(x[nt][c], x[nt][c + 2]);
 #pragma unroll
                     for (int k = 4; k < 32; k <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
-                    m = fmaxf(m + vef, base[nt][c]);
+                    m = fmaxf(m + (vef - kTopNew), base[nt][c]);
                     const float f = base[nt][c] == -INFINITY ? 0.f : exp2f(base[nt][c] - m);
                     base[nt][c] = m;
                     sum[nt][c] *= f;
