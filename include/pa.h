@@ -445,9 +445,9 @@ int pa_gather_runs(const void* src_k, const void* src_v, int src_blocks,
  * For token t at position p = positions[t], every head and pair i = 0 .. rotary_dim/2 - 1, with
  * (a, b) = elements (i, i + rotary_dim/2) of the head, or (2i, 2i + 1) when `interleaved` != 0:
  *   (a, b) -> magnitude * (a cos(p f_i) - b sin(p f_i), b cos(p f_i) + a sin(p f_i)),  f_i = inv_freq[i]
- * Elements rotary_dim .. head_dim-1 are passed on unchanged.  Computed in fp32 and rounded once; the
- * angle is reduced in 64-bit integers (its error is |p| (|f_i| 2^-52 + 2^-62) rad), so that far and
- * negative positions keep fp32's precision.
+ * Elements rotary_dim .. head_dim-1 are passed on unchanged.  Computed in fp32 and rounded once.  The
+ * angle is reduced to [-pi, pi] in 64-bit integers, so that far and negative positions keep fp32's
+ * precision: it is off by |p| (|f_i| 2^-52 + 2^-62) rad, and by 2^-23 of itself where it enters fp32.
  *   q, k, out_q, out_k: [num_tokens][heads][head_dim] 16-bit elements; a token's heads are contiguous,
  *     tokens lie *_stride elements apart (a multiple of 8; an input's may be 0).  out_q may be q and
  *     out_k may be k (same pointer and stride); any other overlap is refused.  num_kv_heads == 0:
