@@ -473,7 +473,8 @@ int pa_rope(void* out_q, void* out_k, const void* q, const void* k, long long ou
  * pa_cache_append_q8  [P4 §三 sequence diagram; P1 address formula]
  * Quantise and write each sequence's new rows: sequence s's n_s rows query_start[s] ..
  * query_start[s+1]-1 of k and v are the tokens at positions L - n_s .. L - 1 of its L = context_lens[s]
- * (counts clamped and flagged as in pa_multi_query); query_start == NULL: row s is the newest token of
+ * (query_start as in pa_multi_query, counts clamped and flagged as there; where it decreases, rows of the
+ * sequences around may be left unwritten); query_start == NULL: row s is the newest token of
  * sequence s (num_tokens == num_seqs; sequences with L == 0 write nothing).  In every (block, kv head)
  * that receives rows, with amax the largest finite |x| of the rows it receives:
  *   e_need = the least e in -60 .. 60 with amax <= 448 * 2^e (60 when there is none, -60 when amax = 0)

@@ -161,6 +161,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kCtas) append_q8_kernel(con
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int B = a.block_size, Hkv = a.num_kv_heads;
     const int part = warp % wpu;                               // of the unit's `wpu` warps
+    // where query_start decreases, the search below may miss the sequences around (the grid has a thread for each)
+    const unsigned tid = blockIdx.x * blockDim.x + threadIdx.x;
+    if (tid < (unsigned)a.num_seqs && a.q_start[tid + 1] < a.q_start[tid]) flag_status(a.status, PA_DEV_BAD_CONTEXT);
     const unsigned u = blockIdx.x * (kAppendWarps / wpu) + warp / wpu;   // (virtual block, head, K or V)
     const int is_v = u % 2, h = (int)(u / 2 % Hkv), v = (int)(u / 2 / Hkv);
     if (v >= blocks) return;

@@ -357,3 +357,15 @@ def test_append_and_read_refuse():
                         (lambda: pa.read_blocks_q8(*c.dev, out, out, lens, lens[:1]), ValueError)):
         with pytest.raises(error):
             call()
+
+
+def test_append_flags_a_query_start_that_decreases():
+    """Not a batch the call takes: some of its rows may stay unwritten, but never without the status word."""
+    for start in ([0, 50, 10, 60], [100, 0, 50], [0, 60, 60, 59, 60]):
+        S = len(start) - 1
+        c = Cache(6 * S, 2, 16, seed=41)
+        k, v = _rows(max(start), 2, torch.float16, seed=42)
+        tables = np.arange(6 * S, dtype=np.int32).reshape(S, 6)
+        c.append(k, v, tables, [65] * S, np.array(start), max_q=64)
+        torch.cuda.synchronize()
+        assert pa.read_device_status(clear=True) == pa._native.DEV_BAD_CONTEXT, start
