@@ -19,7 +19,7 @@
 // read_q8: code * 2^e rounded to the pool's 16-bit type (bf16 exactly), beyond its range to its
 // largest value; one thread per 16 codes of K and of V.
 //
-// Both are bound by HBM: 512 rows x 16 sequences x 32 heads appended in 34 us (32-token blocks; 0.87 of a copy's
+// Both are bound by HBM: 512 rows x 16 sequences x 32 heads appended in 33 us (32-token blocks; 0.89 of a copy's
 // rate), 2048 blocks of 32 rows x 32 heads read back in 241 us (0.98).  One row a sequence (64 x 2 heads) takes
 // 2.2 us: the launch, and length, table and exponent one after another.
 #include <type_traits>
@@ -149,9 +149,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_one_q8_kernel(const 
 }
 
 // kWpu: warps of a unit (0: `warps_per_unit`); kCtas: CTAs that share an SM (their registers: a chunk's append is bound
-// by the bytes in flight, 512 rows x 16 sequences x 32 heads: 35.9 us with 3 in 16-token blocks, 32.9 with 4; 38.8 with
-// 2 in 64-token blocks, 36.3 with 3; a few rows a sequence by the first waits: one to eight rows x 100 sequences, 4.4 us
-// with 3 and 4.8 with 4).
+// by the bytes in flight, 512 rows x 16 sequences x 32 heads: 35.9 us with 3 in 16-token blocks, 32.2 with 4; 36.5 with
+// 2 in 32-token blocks, 33.3 with 3; 38.8 with 2 in 64-token blocks, 35.4 with 3; a few rows a sequence by the first
+// waits: one to eight rows x 100 sequences, 4.1 us with 3 and 4.8 with 4).
 template <typename T, int kRows, int kWpu, int kCtas>
 __global__ void __launch_bounds__(kAppendWarps * 32, kCtas) append_q8_kernel(const AppendQ8Args a, int blocks, int warps_per_unit) {
     const int wpu = kWpu ? kWpu : warps_per_unit;
@@ -167,14 +167,11 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kCtas) append_q8_kernel(con
     const unsigned u = blockIdx.x * (kAppendWarps / wpu) + warp / wpu;   // (virtual block, head, K or V)
     const int is_v = u % 2, h = (int)(u / 2 % Hkv), v = (int)(u / 2 / Hkv);
     if (v >= blocks) return;
-    int s = v, j = 0;
-    if (a.q_start) {
-        s = find_seq(a, v, lane);
-        j = (int)(v - (max(0, min(a.q_start[s], a.rows)) / B + 2LL * s));
-    }
+    const int s = find_seq(a, v, lane);
     bool bad_len;
     const int L = clamped_len(a.context_lens, s, a.max_blocks_per_seq, B, &bad_len);
     const NewRows nr = new_rows(a.q_start, a.rows, a.max_q, s, L);
+    const int j = (int)(v - (nr.row0 / B + 2LL * s));
     const bool speaks = h == 0 && !is_v && part == 0 && lane == 0;
     if ((bad_len || nr.bad) && j == 0 && speaks) flag_status(a.status, PA_DEV_BAD_CONTEXT);
     const int p0 = L - nr.n;                                   // first new position
@@ -332,7 +329,7 @@ static cudaError_t launch_append(const AppendQ8Args& a, cudaStream_t stream) {
             if (a.rows / a.num_seqs >= a.block_size)
                 return launch_pdl(append_q8_kernel<T, 16, 1, 4>, grid, block, 0, stream, a, blocks, 1);
             break;
-        case 32: return launch_pdl(append_q8_kernel<T, 32, 1, 2>, grid, block, 0, stream, a, blocks, 1);
+        case 32: return launch_pdl(append_q8_kernel<T, 32, 1, 3>, grid, block, 0, stream, a, blocks, 1);
     }
     return launch_pdl(append_q8_kernel<T, 16, 1, 3>, grid, block, 0, stream, a, blocks, 1);
 }

@@ -142,7 +142,6 @@ struct NewRows {
 };
 
 __device__ __forceinline__ NewRows new_rows(const int32_t* q_start, int rows, int max_q, int s, int L) {
-    if (!q_start) return NewRows{s, L > 0 ? 1 : 0, false};
     const int b = q_start[s], e = q_start[s + 1];
     const int r0 = max(0, min(b, rows));
     const long long want = (long long)e - b;
