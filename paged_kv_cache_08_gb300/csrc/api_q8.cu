@@ -67,7 +67,7 @@ int pa_rope(void* out_q, void* out_k, const void* q, const void* k, long long ou
     if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads < 0 || head_dim <= 0 || rotary_dim <= 0 ||
         rotary_dim > head_dim)
         return PA_ERR_INVALID_ARG;
-    if (head_dim % 8 || rotary_dim % 16 || head_dim > 1024 || num_q_heads > 65535 || num_kv_heads > 65535)
+    if (head_dim % 8 || rotary_dim % 16 || head_dim > kRopeMaxHead || num_q_heads > 65535 || num_kv_heads > 65535)
         return PA_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PA_OK;
     const bool has_k = num_kv_heads > 0;

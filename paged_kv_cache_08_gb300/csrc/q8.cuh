@@ -15,6 +15,7 @@
 namespace pa {
 
 constexpr int kExpMin = -60, kExpMax = 60;   // sums of two exponents and the softmax's own stay in fp32
+constexpr int kRopeMaxHead = 1024;            // head size of a rotation
 constexpr int kQ8MaxRows = 32;               // query rows per (sequence, kv head) of one attention call
 
 struct RopeArgs {
