@@ -574,8 +574,8 @@ def gather_runs(src_k: torch.Tensor, src_v: torch.Tensor, dst_k: torch.Tensor, d
 # ------------------------------------------------------------------------------------------
 
 # These calls are short on the GPU (microseconds).  Their common case (plain tensors on the current device, the
-# current stream) is checked and passed on in C (csrc/marshal.c), which returns None when a call is any other:
-# the code below then takes it.  It touches each tensor once, its type, device and layout together, and works out
+# current stream) is checked and passed on in C (csrc/marshal.c), which returns None when a call is any other (or where
+# it is not built): the code below then takes it.  It touches each tensor once, its type, device and layout together, and works out
 # the message only when one is wrong.
 
 _marshal = None
@@ -590,6 +590,7 @@ def _in_c():
                 _q8_workspace)
         _marshal = m
     return _marshal
+
 
 def _want(name: str, t, dtype, dev: int) -> int:
     """The address of a contiguous tensor of ``dtype`` on CUDA device ``dev``."""

@@ -1,4 +1,5 @@
-"""Build libpa.so (CUDA kernels + C ABI + host pool) for sm_103a and the binding's C part, in-tree.
+"""Build libpa.so (CUDA kernels + C ABI + host pool) for sm_103a and the binding's C part, in-tree.  The latter needs gcc
+and Python's headers; without them it is left out, and the binding's Python code makes all calls.
 
     python -m paged_kv_cache_08_gb300.build [--force]
 
@@ -8,11 +9,13 @@ under csrc/ or include/ is newer than its object file.
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
+from typing import Optional
 
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
@@ -20,7 +23,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 LIB = BUILD / "libpa.so"
-MARSHAL = BUILD / "_marshal.so"
+MARSHAL = BUILD / ("_marshal" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))   # one for each interpreter version
 
 CUDA_SOURCES = ["api.cu", "api_q8.cu", "cache_q8.cu", "cache_write.cu", "copy_blocks.cu", "decode_fma.cu", "decode_mma.cu",
                 "decode_persist.cu", "decode_planned.cu", "decode_q8.cu", "decode_static.cu",
@@ -75,18 +78,31 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> Path:
         if r.returncode != 0:
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    src = CSRC / "marshal.c"
-    if force or not MARSHAL.exists() or MARSHAL.stat().st_mtime < max(src.stat().st_mtime, hdr):
-        tmp = BUILD / f"_marshal.so.tmp{os.getpid()}"
-        cmd = ["gcc", "-O2", "-fPIC", "-shared", "-Wall", "-I", sysconfig.get_paths()["include"], str(src), "-o", str(tmp),
-               "-L", str(BUILD), "-lpa", "-Wl,-rpath,$ORIGIN"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-        if r.stderr.strip():
-            sys.stderr.write(r.stderr)
-        os.replace(tmp, MARSHAL)
+    build_marshal(force)
     return LIB
+
+
+def build_marshal(force: bool = False) -> Optional[Path]:
+    """The binding's C part, or None where it cannot be built."""
+    src = CSRC / "marshal.c"
+    if not force and MARSHAL.exists() and MARSHAL.stat().st_mtime >= max(src.stat().st_mtime, _headers_mtime()):
+        return MARSHAL
+    include = Path(sysconfig.get_paths()["include"])
+    missing = [what for what, there in (("gcc", shutil.which("gcc")), (f"{include}/Python.h", (include / "Python.h").exists()))
+               if not there]
+    if missing:
+        sys.stderr.write(f"{MARSHAL.name} is left out (no {', no '.join(missing)}): short calls take longer on the host\n")
+        return None
+    tmp = BUILD / f"{MARSHAL.name}.tmp{os.getpid()}"
+    cmd = ["gcc", "-O2", "-fPIC", "-shared", "-Wall", "-I", str(include), str(src), "-o", str(tmp), "-L", str(BUILD), "-lpa",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    if r.stderr.strip():
+        sys.stderr.write(r.stderr)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 if __name__ == "__main__":

@@ -8,8 +8,12 @@ import subprocess
 import sysconfig
 from pathlib import Path
 
+import numpy as np
 import pytest
 import torch
+
+import paged_kv_cache_08_gb300 as pa
+from paged_kv_cache_08_gb300 import _native, build
 
 ROOT = Path(__file__).resolve().parent.parent
 STAND_IN = """
@@ -123,3 +127,64 @@ def test_a_tensor_without_an_address_is_left_to_python(native, device0, call, at
 
     torch.vmap(body)(torch.stack([args[at].view(torch.uint8)] * 2).view(args[at].dtype))
     assert results == [None] and calls.value == 0
+
+
+def test_the_built_file_is_this_interpreters():
+    assert build.MARSHAL == _native.MARSHAL_PATH
+    assert build.MARSHAL.name == "_marshal" + sysconfig.get_config_var("EXT_SUFFIX")
+
+
+@pytest.mark.parametrize("lacks", ["headers", "gcc"])
+def test_the_build_goes_on_without_headers_or_compiler(monkeypatch, tmp_path, capsys, lacks):
+    monkeypatch.setattr(build, "MARSHAL", tmp_path / "_marshal.so")
+    if lacks == "headers":
+        monkeypatch.setattr(build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    else:
+        monkeypatch.setattr(build.shutil, "which", lambda name: None)
+    assert build.build_marshal() is None
+    assert not build.MARSHAL.exists()
+    assert ("Python.h" if lacks == "headers" else "gcc") in capsys.readouterr().err
+
+
+@pytest.fixture()
+def not_built(monkeypatch, tmp_path):
+    monkeypatch.setattr(_native, "MARSHAL_PATH", tmp_path / "_marshal.so")
+    monkeypatch.setattr(pa, "_marshal", None)
+
+
+def test_calls_are_made_without_it(not_built):
+    """Refused by the Python code's checks, not for the missing file."""
+    h = torch.zeros((4, 2, 128), dtype=torch.float16)
+    with pytest.raises(TypeError):
+        pa.rope(h, None, torch.zeros(4, dtype=torch.int32), torch.zeros(64, dtype=torch.float64))
+    assert isinstance(pa._marshal, _native.PythonCalls)
+
+
+@pytest.mark.gpu
+def test_results_are_the_same_without_it(monkeypatch):
+    dev = torch.device("cuda")
+    gen = torch.Generator(device=dev).manual_seed(3)
+    f, _ = pa.rope_frequencies(128)
+    lens = torch.tensor([37, 5, 64], dtype=torch.int32, device=dev)
+    tables = torch.arange(12, dtype=torch.int32, device=dev).reshape(3, 4)
+    start = torch.tensor([0, 3, 5, 6], dtype=torch.int32, device=dev)
+    q = torch.randn((6, 12, 128), generator=gen, device=dev).half()
+    k, v = (torch.randn((6, 2, 128), generator=gen, device=dev).half() for _ in range(2))
+
+    def step():
+        cache = [torch.zeros((12, 2, 16, 128), device=dev).to(torch.float8_e4m3fn) for _ in range(2)]
+        cache += [torch.zeros((12, 2), dtype=torch.int8, device=dev) for _ in range(2)]
+        a, b = pa.rope(q, k, torch.arange(6, device=dev), f)
+        pa.cache_append_q8(b, v, *cache, tables, lens, start, 3)
+        pa.cache_append_q8(b[:3], v[:3], *cache, tables, lens)
+        out = [a, b, pa.multi_query_q8(a, *cache, tables, lens, start, 0.1, 2, 3),
+               pa.decode_q8(a[:3], *cache, tables, lens, 0.1, 2)]
+        back = [torch.zeros((12, 2, 16, 128), dtype=torch.float16, device=dev) for _ in range(2)]
+        pa.read_blocks_q8(*cache, *back, tables.flatten(), tables.flatten())
+        torch.cuda.synchronize()
+        return [np.asarray(x.cpu().view(torch.uint8)) for x in out + cache + back]
+
+    want = step()
+    monkeypatch.setattr(pa, "_marshal", _native.PythonCalls())
+    for a, b in zip(step(), want):
+        assert np.array_equal(a, b)
