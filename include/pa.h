@@ -468,7 +468,8 @@ int pa_rope(void* out_q, void* out_k, const void* q, const void* k, long long ou
  * in block b, kv head h is c * 2^e, e = exp[b][h] (read as clamped to -60 .. 60): one power-of-two
  * scale for each block of tokens and head.  Head size 128, block_size 16/32/64/128.  Whole blocks are
  * copied by pa_copy_blocks on the pools seen as 16-bit elements of head size 64, with their exponents
- * copied by the caller.
+ * copied by the caller.  At most 65535 sequences and kv heads, 2^30 tokens a table row and
+ * num_blocks x num_kv_heads x block_size < 2^31, else PA_ERR_UNSUPPORTED.
  *
  * pa_cache_append_q8  [P4 §三 sequence diagram; P1 address formula]
  * Quantise and write each sequence's new rows: sequence s's n_s rows query_start[s] ..

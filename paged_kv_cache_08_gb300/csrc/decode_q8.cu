@@ -35,10 +35,12 @@
 // most tiles need no shuffle.
 //
 // Bound by HBM (one byte per cached element) with up to 8 rows a segment: 16 contexts of 16384 tokens, 8 kv heads of
-// 4 rows 86 us (6.2 TB/s, 0.92 of a copy's rate), 256 short chats of 32 heads 58 us (5.2 TB/s).  With more rows by
-// the issue slots: 272 instructions a tile of 8 rows, 348 of 16, 541 of 32, about 0.36 a cycle and scheduler (two
-// warps each, waiting for their own products); the long contexts then take 105 us with 16 rows and 159 with 32.  The
-// smallest calls are a chain of latencies: four short contexts 6.2 us, 64 sequences of 16 to 2048 tokens 12.6 us.
+// 4 rows 86 us (6.2 TB/s, 0.92 of a copy's rate), 256 short chats of 32 heads 58 us (5.2 TB/s).  With more rows by the
+// warps' waits for their own products: a tile of 32 rows fills a warp's registers, so that a scheduler has two warps,
+// each in one chain of dependent steps (272 instructions a tile of 8 rows, 348 of 16, 541 of 32, about 0.36 a cycle and
+// scheduler; waits of a fixed latency are the largest stall, two warps an issue).  The long contexts take 104 us with 16
+// rows, 131 with 24 and 164 with 32.  The smallest calls are a chain of latencies: four short contexts 6.2 us, 64
+// sequences of 16 to 2048 tokens 12.7 us.
 #include <atomic>
 #include <type_traits>
 
