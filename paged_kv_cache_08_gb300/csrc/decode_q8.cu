@@ -39,7 +39,7 @@
 // warps' waits for their own products: a tile of 32 rows fills a warp's registers, so that a scheduler has two warps,
 // each in one chain of dependent steps (272 instructions a tile of 8 rows, 348 of 16, 541 of 32, about 0.36 a cycle and
 // scheduler; waits of a fixed latency are the largest stall, two warps an issue).  The long contexts take 104 us with 16
-// rows, 131 with 24 and 164 with 32.  The smallest calls are a chain of latencies: four short contexts 6.2 us, 64
+// rows, 131 with 24 and 163 with 32.  The smallest calls are a chain of latencies: four short contexts 6.2 us, 64
 // sequences of 16 to 2048 tokens 12.7 us.
 #include <atomic>
 #include <type_traits>
@@ -64,7 +64,8 @@ __host__ __device__ constexpr int start_units(int rows) { return rows > 16 ? 3 :
 constexpr int kQ8MaxSeqs = 1024;                // sequences of one launch (their lengths stay on chip)
 // log2 of P: a new base puts the largest at 2^kTopNew, and moves when one would exceed 2^kTopMost (fp16's largest is
 // below 2^16).  9 is the highest that costs nothing: one to five new tokens 22.8 us with 7 and 9, 23.5 with 11, 24.7
-// with 13, since the base then moves more often.
+// with 13, since the base then moves more often.  (Scores of 2^24 and more leave few bits for such offsets: the distance
+// to the base, not the sum with it, is compared, and a new base is rounded up.)
 constexpr float kTopNew = 9.f, kTopMost = 15.f;
 
 // Floats of a piece of `rows` rows: O, then (base, sum) of each row; a multiple of 16 bytes.
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
 #pragma unroll
         for (int nt = 0; nt < K; ++nt)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) move |= fmaxf(x[nt][c], x[nt][c + 2]) > base[nt][c] + slack;
+            for (int c = 0; c < 2; ++c) move |= fmaxf(x[nt][c], x[nt][c + 2]) - base[nt][c] > slack;
         if (__any_sync(kAll, move)) {
 #pragma unroll
             for (int nt = 0; nt < K; ++nt)
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(Q8Smem<NT, kW>::kThreads, 1)
                     float m = fmaxf(x[nt][c], x[nt][c + 2]);
 #pragma unroll
                     for (int k = 4; k < 32; k <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
-                    m = fmaxf(m + (vef - kTopNew), base[nt][c]);
+                    m = fmaxf(__fadd_ru(m, vef - kTopNew), base[nt][c]);   // never below: P must stay in range
                     const float f = base[nt][c] == -INFINITY ? 0.f : exp2f(base[nt][c] - m);
                     base[nt][c] = m;
                     sum[nt][c] *= f;

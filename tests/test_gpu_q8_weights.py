@@ -99,3 +99,38 @@ def test_weights_at_the_top_of_their_range(scale):
     want, bound = _expect(ref.f64(q[0]), ref.CODE_VALUES[k], ref.CODE_VALUES[v], np.ones(L), vs, scale)
     ref.check_attention(out, want[None], bound[None], np.ones(1, dtype=bool))
     assert math.isfinite(float(out.float().abs().max())) or (np.abs(want) > 65504).any()
+
+
+@pytest.mark.parametrize("log2_top", [20, 23, 24, 25, 26, 27])
+@pytest.mark.parametrize("v_exp", [-20, 0, 14])
+@pytest.mark.parametrize("dtype,new", [(torch.float16, 0), (torch.bfloat16, 0), (torch.float16, 3)])
+def test_scores_too_large_for_their_differences(dtype, new, v_exp, log2_top):
+    """Scores of 2^20 to 2^27 that differ by a few units: fp32 holds their differences in steps of up to 16, so that the
+    weights are nobody's to say, but every output is a mean of V's values, which lie in [1, 1.875] x 2^v_exp."""
+    L, block = 1500, 16
+    nb = -(-L // block)
+    rng = np.random.default_rng(log2_top)
+    k = np.zeros((nb * block, ref.D), dtype=np.uint8)
+    k[:, 0] = ref.to_code(np.array(256.0))
+    k[:, 1] = ref.to_code(np.linspace(0, 400, nb * block))          # climbing differences
+    k[:, 2] = ref.to_code(rng.uniform(-16, 16, nb * block))
+    v = ref.to_code(rng.integers(8, 16, (nb * block, ref.D)) / 8.0)
+    rows = max(1, new)
+    q = torch.zeros((rows, 5, ref.D), dtype=dtype)
+    q[:, :, 0] = 2.0 ** 10
+    q[:, :, 1:3] = torch.tensor([0.25, 0.5, 1.0, 2.0, 4.0])[:, None] * 2.0 ** (18 - log2_top)
+    scale = 2.0 ** (log2_top - 18)
+    pool = lambda c: torch.from_numpy(c.reshape(nb, 1, block, ref.D)).to(DEV).view(torch.float8_e4m3fn)  # noqa: E731
+    exps = [torch.full((nb, 1), e, dtype=torch.int8, device=DEV) for e in (0, v_exp)]
+    args = [q.to(DEV), pool(k), pool(v), *exps, torch.arange(nb, dtype=torch.int32, device=DEV)[None],
+            torch.tensor([L], dtype=torch.int32, device=DEV)]
+    if new:
+        out = pa.multi_query_q8(*args, torch.tensor([0, new], dtype=torch.int32, device=DEV), scale, 1, new)
+    else:
+        out = pa.decode_q8(*args, scale, 1)
+    torch.cuda.synchronize()
+    y = ref.f64(out) * 2.0 ** -v_exp
+    # a weight's rounding to fp16 (2^-11 of it, or a step below 2^-14 beside a largest one of 2^(9 - 16) at least) and
+    # the output's own (2^-8 in bf16, in fp16's subnormals 2^-25 x 2^20)
+    assert np.isfinite(y).all()
+    assert y.min() >= 1 - 2.0 ** -4 and y.max() <= 1.875 + 2.0 ** -4
