@@ -523,7 +523,8 @@ int pa_read_blocks_q8(const void* k_cache, const void* v_cache, const int8_t* k_
  * PA_DEV_BAD_BLOCK_ID (a row with no token left is zero).
  * Cached rows at positions >= L, and table entries behind them, do not affect the result.
  * max_q_per_seq x (num_q_heads / num_kv_heads) <= 32 (pa_decode_q8: max_q_per_seq = 1), else
- * PA_ERR_UNSUPPORTED; longer chunks: pa_read_blocks_q8, then pa_multi_query.
+ * PA_ERR_UNSUPPORTED; longer chunks: pa_read_blocks_q8, then pa_multi_query (up to 64 rows two calls are
+ * faster, the first of the earlier tokens over contexts that end with them).
  * workspace: pa_decode_q8_workspace_size(...) bytes of device memory, 16-byte aligned, caller-owned; its
  * contents before the call do not matter.  Calls that share a workspace must not overlap on the GPU.
  * Returns the codes of pa_decode.
