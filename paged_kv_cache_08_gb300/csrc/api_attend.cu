@@ -47,7 +47,10 @@ Dispatch dispatch(int num_seqs, int num_q_tokens, int max_q, int num_q_heads, in
                   int max_blocks_per_seq, int num_groups, int max_prefix_blocks) {
     Dispatch d;
     const int group = num_q_heads / num_kv_heads, sms = sm_count_current();
+    // Query rows of all sequences, whose counts the kernels clamp, and of all groups, whose tiles lie over all rows from the
+    // first sequence's to the last one's, those that a clamped count leaves out among them.
     const long long rows = min((long long)num_q_tokens, (long long)num_seqs * max_q) * group;
+    const long long group_rows = (long long)num_q_tokens * group;
     const long long keys = (long long)max_blocks_per_seq * block_size, prefix = (long long)max_prefix_blocks * block_size;
     d.stream = (long long)group * max_q <= kStreamRows;
     // Where the tables bound all contexts together to 16 MB, reading the prefix for every sequence costs less than the
@@ -64,7 +67,7 @@ Dispatch dispatch(int num_seqs, int num_q_tokens, int max_q, int num_q_heads, in
             // stage takes a CTA with two tiles 1.1 us, a streaming CTA reads 60 KB in 1 us with up to 8 rows a segment and
             // half of that with more, all together 6 GB/s; half the rest of the tables is taken for the tails' length,
             // which is not known here.
-            const TcSplits one = tc_splits(rows, num_groups, num_kv_heads, prefix, 1, sms);
+            const TcSplits one = tc_splits(group_rows, num_groups, num_kv_heads, prefix, 1, sms);
             const double stages = (double)one.items * num_kv_heads * (double)(prefix / 64 + 1);
             const bool few = group * max_q <= 8;
             const double kb = (group * max_q > kSegmentRows ? 1.0 : 0.5) * num_kv_heads * num_seqs *
@@ -79,7 +82,7 @@ Dispatch dispatch(int num_seqs, int num_q_tokens, int max_q, int num_q_heads, in
             }
             tc_sms = sms - most;
         }
-        d.prefix = tc_splits(rows, num_groups, num_kv_heads, prefix, kMostPrefix, tc_sms);
+        d.prefix = tc_splits(group_rows, num_groups, num_kv_heads, prefix, kMostPrefix, tc_sms);
     }
     if (!d.stream) d.own = tc_splits(rows, num_seqs, num_kv_heads, keys, kMostOwn, sms);
     d.stream_ctas = d.stream ? stream_ctas(num_seqs, num_kv_heads, group * max_q, block_size, max_blocks_per_seq, most) : 0;
