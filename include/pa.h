@@ -568,10 +568,10 @@ size_t pa_decode_q8_workspace_size(int num_seqs, int num_q_heads, int num_kv_hea
  * first_key begins a row's document or its window, and the first bidirectional[s] tokens (an image, a prompt) are seen
  * by every row.  A row that sees no token is zero.  cap: 0 (none) or positive.  slopes: float [num_q_heads];
  * first_key: int32, one per row of q; bidirectional: int32 [num_seqs]; each NULL for none; device memory.
- * Products and sums in fp32, rounded once into `dtype`; the softmax weights enter the PV product with 11 bits (fp16) or, for
- * bf16, 16 up to 32 rows a kv head (below) and 8 beyond, where their sum is that of the rounded ones.  Tokens that a row does not see do not affect it, whatever their K and V hold.  Rows that no sequence owns
- * are neither read nor written.  Tokens of a block whose table entry lies outside the pool are left out of the softmax
- * and set PA_DEV_BAD_BLOCK_ID.  pa_decode_scored: one query row per sequence, at position L - 1; L == 0 gives a zero row.
+ * Products and sums in fp32, rounded once into `dtype`; the softmax weights enter the PV product with 11 bits (fp16) or 16
+ * (bf16: a high and a low part).  Tokens that a row does not see do not affect it, whatever their K and V hold.  Rows
+ * that no sequence owns are neither read nor written.  Tokens of a block whose table entry lies outside the pool are left
+ * out of the softmax and set PA_DEV_BAD_BLOCK_ID.  pa_decode_scored: one query row per sequence, at position L - 1; L == 0 gives a zero row.
  * Kernels: while max_q_per_seq x (num_q_heads / num_kv_heads) <= 32 warps that stream equal shares of all tokens some
  * row sees; beyond that tcgen05 tiles of 128 query rows.  Head size 128, block_size 16/32/64/128, at most 65535
  * sequences and query heads and 32767 kv heads, 2^30 tokens a table row, num_blocks x num_kv_heads x block_size and

@@ -13,7 +13,7 @@
 //   warp 8          copies of 64-token K and V stages into a ring of four
 //   warps 9, 10     products of tile 0, tile 1: S = Q K^T, O += P V (P in tensor memory), issued by one lane each
 //   warp 11         makes a stage's V fit for products with weights of zero (below)
-// Tensor memory and the order of its buffers are those of prefill_tc.cu (two P buffers for both types).
+// Tensor memory and the order of its buffers are those of prefill_tc.cu.
 //
 // Masks: every row has an interval of keys.  Stages that no row of the CTA sees are not read, a tile passes over those
 // that none of its rows sees, and where every row of a warp sees a whole stage there is nothing to mask.  A masked weight
@@ -23,7 +23,8 @@
 //
 // Caps: tanh is a polynomial on the FMA units while every score of a warp's stage stays within 3/4 of the cap, else
 // 1 - 2 / (1 + e^2y) on the special-function unit, which the softmax's own exponentials already fill.
-// P is rounded to the cache's type; bf16's weights (8 bits) are summed as rounded.
+// P is rounded to fp16, or taken as a high and a low bf16 part (two products): 8 bits of a weight would be the largest error
+// of the result.
 //
 // What bounds it: a CTA's stage of 64 tokens (two tiles) takes 2050 cycles without options, of which its products need
 // 1024 and the shared memory that feeds them about 1540 (Q is read again for every 64 keys, K and V by both tiles); the
@@ -67,7 +68,7 @@ constexpr size_t kSmem = 1024 + kOffMisc + kMiscInts * 4;
 static_assert(kSmem <= 227 * 1024, "one CTA's shared memory must fit in 227 KB");
 constexpr uint32_t kTmemCols = 512;                          // per tile: S at +0, P at +64, O at +128
 constexpr uint32_t kTileCols = 256;
-constexpr uint32_t kColP = 64, kColO = 128;
+constexpr uint32_t kColP = 64, kColO = 128;                  // P: fp16 two buffers in turn, bf16 the high and the low part
 // log2 of P: a new base puts the largest at 2^top_new, and moves when one would exceed 2^top_most.  fp16: weights keep 11
 // bits down to 2^-19 of the row's largest and steps of 2^-29 of it below.  (A move costs about 1000 cycles, for it waits for
 // the tile's products; with 2^8 between the two one stage in four of a warp moved, scores of standard deviation 4.)
@@ -215,6 +216,7 @@ __device__ __forceinline__ Unit unit_of(const TcLaunch& p, int u) {
 template <typename T, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kTThreads, 1)
     attend_tc_kernel(const TcLaunch p, const __grid_constant__ Maps maps) {
+    constexpr bool kSplitP = std::is_same<T, __nv_bfloat16>::value;
     extern __shared__ unsigned char smem_raw[];
     const AttendArgs& a = p.a;
     const uint32_t raw = smem_u32(smem_raw);
@@ -605,12 +607,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 }
                 tc_fence_after();
                 const uint64_t dv = dv0 + (uint64_t)(((uint32_t)sl * kStage) >> 4);
-                const uint32_t pt = d + kColP + (uint32_t)(k & 1) * 32u;
+                const uint32_t pt = d + kColP + (kSplitP ? 0u : (uint32_t)(k & 1) * 32u);
                 if (elect_one()) {
 #pragma unroll
-                    for (int kt = 0; kt < 4; ++kt)
-                        umma_ts(d + kColO, pt + (uint32_t)(kt * 8), dv + (uint64_t)((kt * 2048) >> 4), kIdPV,
-                                (k > 0 || kt > 0) ? 1u : 0u);
+                    for (int kt = 0; kt < 4; ++kt) {
+                        const uint64_t v = dv + (uint64_t)((kt * 2048) >> 4);
+                        umma_ts(d + kColO, pt + (uint32_t)(kt * 8), v, kIdPV, (k > 0 || kt > 0) ? 1u : 0u);
+                        if (kSplitP) umma_ts(d + kColO, pt + 32u + (uint32_t)(kt * 8), v, kIdPV, 1u);
+                    }
                     bar_commit(pv_done + (t * 2 + (k & 1)) * 8);
                     bar_commit(kv_empty + sl * 8);
                 }
@@ -843,21 +847,42 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
             const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
             float2 rs2[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-            uint32_t w[32];
+            // P goes to tensor memory in parts of kPart words.  fp16: the buffer was last read by the product of two stages
+            // before, which was issued before this stage's S: it is complete, since the arrival on s_full waits for all that
+            // was issued before it.  bf16: the one buffer is free once the last stage's product is complete.
+            constexpr int kPart = kSplitP ? 16 : 32;
+            const uint32_t p_at = lane_addr + kColP + (kSplitP ? 0u : (uint32_t)(k & 1) * 32u);
             auto weights = [&](auto exponent, auto masked) {
 #pragma unroll
-                for (int c2 = 0; c2 < 32; ++c2) {
-                    const float2 e2 = exponent(c2, make_float2(x[2 * c2], x[2 * c2 + 1]));
-                    float p0 = ex2(e2.x);
-                    float p1 = ex2(e2.y);
-                    if (decltype(masked)::value) {
-                        p0 = vis[c2 >> 4] & (1u << (2 * c2 & 31)) ? p0 : 0.f;
-                        p1 = vis[c2 >> 4] & (2u << (2 * c2 & 31)) ? p1 : 0.f;
+                for (int part = 0; part < 32; part += kPart) {
+                    uint32_t w[kPart], low[kPart];
+#pragma unroll
+                    for (int c = 0; c < kPart; ++c) {
+                        const int c2 = part + c;
+                        const float2 e2 = exponent(c2, make_float2(x[2 * c2], x[2 * c2 + 1]));
+                        float p0 = ex2(e2.x);
+                        float p1 = ex2(e2.y);
+                        if (decltype(masked)::value) {
+                            p0 = vis[c2 >> 4] & (1u << (2 * c2 & 31)) ? p0 : 0.f;
+                            p1 = vis[c2 >> 4] & (2u << (2 * c2 & 31)) ? p1 : 0.f;
+                        }
+                        w[c] = Elem<T>::pack2(p0, p1);
+                        if (kSplitP) {
+                            const float2 d = fadd2(make_float2(p0, p1), Elem<T>::to_float2(w[c] ^ 0x80008000u));   // p - w
+                            low[c] = Elem<T>::pack2(d.x, d.y);
+                        }
+                        rs2[c2 & 3] = fadd2(rs2[c2 & 3], make_float2(p0, p1));
                     }
-                    w[c2] = Elem<T>::pack2(p0, p1);
-                    // bf16's weights are summed as they were rounded, so that their common error cancels in O / l
-                    rs2[c2 & 3] = fadd2(rs2[c2 & 3], std::is_same<T, __nv_bfloat16>::value ? Elem<T>::to_float2(w[c2])
-                                                                                          : make_float2(p0, p1));
+                    if constexpr (kSplitP) {
+                        if (part == 0 && k > 0) {
+                            if (!warp_wait(t_pv_done + ((k - 1) & 1) * 8, (uint32_t)((k - 1) >> 1) & 1u)) dead = true;
+                            tc_fence_after();
+                        }
+                        tmem_st16u(p_at + part, w);
+                        tmem_st16u(p_at + 32 + part, low);
+                    } else {
+                        tmem_st32u(p_at, w);
+                    }
                 }
             };
             const float2 nm2 = make_float2(-m_use, -m_use);
@@ -875,9 +900,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             } else {
                 weights([&](int, float2 s) { return ffma2(s, capped2(s), nm2); }, std::true_type{});
             }
-            // The P buffer was last read by the product of two stages before, which was issued before this stage's S: it is
-            // complete, since the arrival on s_full waits for all that was issued before it.
-            tmem_st32u(lane_addr + kColP + (uint32_t)(k & 1) * 32u, w);
+            if (dead) break;
             l_run += ((rs2[0].x + rs2[0].y) + (rs2[1].x + rs2[1].y)) + ((rs2[2].x + rs2[2].y) + (rs2[3].x + rs2[3].y));
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before();
