@@ -70,12 +70,14 @@ constexpr uint32_t kTmemCols = 512;                          // per tile: S at +
 constexpr uint32_t kTileCols = 256;
 constexpr uint32_t kColP = 64, kColO = 128;                  // P: fp16 two buffers in turn, bf16 the high and the low part
 // log2 of P: a new base puts the largest at 2^top_new, and moves when one would exceed 2^top_most.  fp16: weights keep 11
-// bits down to 2^-19 of the row's largest and steps of 2^-29 of it below.  (A move costs about 1000 cycles, for it waits for
-// the tile's products; with 2^8 between the two one stage in four of a warp moved, scores of standard deviation 4.)
+// bits down to 2^-19 of the row's largest and steps of 2^-29 of it below.  bf16 has fp32's range, and O = sum P V must stay
+// in it, too: weights up to 2^8 leave room for |V| up to 2^118, and from 2^-40 on for |V| down to 2^-80.  (A move costs about
+// 1000 cycles, for it waits for the tile's products; with 2^8 between the two one stage in four of a warp moved, scores of
+// standard deviation 4, and a steep bias moves the base every few stages: prompts with one 290 us with 2^24, 280 with 2^48.)
 template <typename T>
-__host__ __device__ constexpr float top_new() { return std::is_same<T, __half>::value ? 5.f : 0.f; }
+__host__ __device__ constexpr float top_new() { return std::is_same<T, __half>::value ? 5.f : -40.f; }
 template <typename T>
-__host__ __device__ constexpr float top_most() { return std::is_same<T, __half>::value ? 15.9f : 60.f; }
+__host__ __device__ constexpr float top_most() { return std::is_same<T, __half>::value ? 15.9f : 8.f; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kAll = 0xffffffffu;
 

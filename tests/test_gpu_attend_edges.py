@@ -31,6 +31,31 @@ def as_single_tokens(case):
     return one, rows
 
 
+def copies(case, n):
+    """The batch n times over the same blocks: so many rows that no row's keys are split among CTAs."""
+    S = len(case["lens"])
+    many = dict(case, q=case["q"].repeat(n, 1, 1), tables=case["tables"].repeat(n, 1), lens=case["lens"].repeat(n))
+
+    def ends(x, step):
+        return torch.cat([x[:1]] + [x[1:] + i * step for i in range(n)]).to(torch.int32)
+
+    if case["start"] is not None:
+        many["start"] = ends(case["start"], int(case["start"][-1]))
+    if case.get("first") is not None:
+        many["first"] = case["first"].repeat(n)
+    if case.get("group_start") is not None:   # (the groups hold all sequences)
+        many.update(prefix_tables=case["prefix_tables"].repeat(n, 1), prefix_lens=case["prefix_lens"].repeat(n),
+                    group_start=ends(case["group_start"], S))
+    return many
+
+
+def check_copies(case, n=160):
+    out = run(copies(case, n)).reshape(n, *case["q"].shape)
+    assert torch.isfinite(out).all()
+    for i in (0, n // 2, n - 1):            # (shares of a stream are cut anywhere: copies differ in their last bits)
+        ref.check(out[i], case)
+
+
 # ---- counts above max_q ----------------------------------------------------------------------
 
 @pytest.mark.parametrize("Hq,Hkv,max_q,new,groups", [
@@ -120,3 +145,30 @@ def test_bf16_weights_just_below_one(kind):
     if kind == "many heads":
         return split_heads(out, case)
     ref.check(out[rows], one)
+
+
+# ---- values and scores of any size -----------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["single", "several", "chunk", "shared", "shared several"])
+@pytest.mark.parametrize("cap", [0.0, 1000.0])
+@pytest.mark.parametrize("size", [2.0 ** 108, 2.0 ** -80])
+@pytest.mark.parametrize("rise", [0.0, 38.0])
+def test_values_of_any_size(kind, cap, size, rise):
+    """bf16 values of about 2^109 and 2^-80 under scores that grow by 38 (55 in log2 units) along the context, or do not."""
+    new = dict(several=[3], chunk=[64]).get(kind, [2, 3] if kind == "shared several" else None)
+    shared = "shared" in kind
+    if shared and cap:
+        return
+    case = make([300, 300] if shared else [300], new, Hq=2, Hkv=1, dtype=BF16, seed=6, groups=[(0, 2, 250)] if shared else None)
+    case["cap"], case["scale"] = cap, rise / 128
+    case["q"][:] = 1.0
+    t = torch.arange(300)
+    for table, n in [(row, 300) for row in case["tables"]] + [(row, 250) for row in case.get("prefix_tables", [])]:
+        case["k_cache"][table.long()[t[:n] // 16], 0, t[:n] % 16] = (t[:n] / 300).bfloat16()[:, None]
+    case["v_cache"] = (case["v_cache"].double() * size).bfloat16()
+    if shared:
+        for s in range(2):                  # the whole last block of the prefix, as its own rows
+            n = 250 % 16
+            src, dst = int(case["prefix_tables"][0, 15]), int(case["tables"][s, 15])
+            case["v_cache"][dst, :, :n] = case["v_cache"][src, :, :n]
+    check_copies(case)
