@@ -70,12 +70,12 @@ constexpr uint32_t kTmemCols = 512;                          // per tile: S at +
 constexpr uint32_t kTileCols = 256;
 constexpr uint32_t kColP = 64, kColO = 128;                  // P: fp16 two buffers in turn, bf16 the high and the low part
 // log2 of P: a new base puts the largest at 2^top_new, and moves when one would exceed 2^top_most.  fp16: weights keep 11
-// bits down to 2^-19 of the row's largest and steps of 2^-29 of it below.  bf16 has fp32's range, and O = sum P V must stay
+// bits down to 2^-21 of the row's largest and steps of 2^-31 of it below.  bf16 has fp32's range, and O = sum P V must stay
 // in it, too: weights up to 2^8 leave room for |V| up to 2^118, and from 2^-40 on for |V| down to 2^-80.  (A move costs about
 // 1000 cycles, for it waits for the tile's products; with 2^8 between the two one stage in four of a warp moved, scores of
 // standard deviation 4, and a steep bias moves the base every few stages: prompts with one 290 us with 2^24, 280 with 2^48.)
 template <typename T>
-__host__ __device__ constexpr float top_new() { return std::is_same<T, __half>::value ? 5.f : -40.f; }
+__host__ __device__ constexpr float top_new() { return std::is_same<T, __half>::value ? 7.f : -40.f; }
 template <typename T>
 __host__ __device__ constexpr float top_most() { return std::is_same<T, __half>::value ? 15.9f : 8.f; }
 constexpr float kLog2e = 1.4426950408889634f;
@@ -854,10 +854,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
             // was issued before it.  bf16: the one buffer is free once the last stage's product is complete.
             constexpr int kPart = kSplitP ? 16 : 32;
             const uint32_t p_at = lane_addr + kColP + (kSplitP ? 0u : (uint32_t)(k & 1) * 32u);
+            uint32_t w[kPart];
             auto weights = [&](auto exponent, auto masked) {
 #pragma unroll
                 for (int part = 0; part < 32; part += kPart) {
-                    uint32_t w[kPart], low[kPart];
+                    uint32_t low[kPart];
 #pragma unroll
                     for (int c = 0; c < kPart; ++c) {
                         const int c2 = part + c;
@@ -882,8 +883,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         }
                         tmem_st16u(p_at + part, w);
                         tmem_st16u(p_at + 32 + part, low);
-                    } else {
-                        tmem_st32u(p_at, w);
                     }
                 }
             };
@@ -902,7 +901,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
             } else {
                 weights([&](int, float2 s) { return ffma2(s, capped2(s), nm2); }, std::true_type{});
             }
-            if (dead) break;
+            if (kSplitP && dead) break;
+            if constexpr (!kSplitP) tmem_st32u(p_at, w);
             l_run += ((rs2[0].x + rs2[0].y) + (rs2[1].x + rs2[1].y)) + ((rs2[2].x + rs2[2].y) + (rs2[3].x + rs2[3].y));
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before();

@@ -147,6 +147,29 @@ def test_bf16_weights_just_below_one(kind):
     ref.check(out[rows], one)
 
 
+@pytest.mark.parametrize("new", [None, [3], [40]])
+def test_fp16_weights_far_below_the_largest(new):
+    """2000 tokens of weight 22.5 * 2^-29 beside one of weight 1 and value 0: a weight is off by no more than 2^-32, half a
+    step of fp16's smallest numbers with the largest weight at 2^7 or more."""
+    case = make([2000], new, Hq=2, Hkv=1, block=128, seed=8)
+    case["q"][:] = 0.25
+    case["k_cache"][:] = 0
+    at = (int(case["tables"][0, 3]), 0, 5)
+    case["k_cache"][at] = 4.0
+    case["scale"] = math.log(2.0 ** 29 / 22.5) / 128
+    case["v_cache"][:] = 1.0
+    case["v_cache"][at] = 0
+    n = 160
+    out = run(copies(case, n)).reshape(n, -1, 2, 128).cpu().double()
+    tail = torch.arange(2000 - out.shape[1], 2000)[:, None, None].double()
+    w = 22.5 * 2.0 ** -29
+    want = tail * w / (1 + tail * w)
+    # Products and sums of the score are exact (0.25 * 4 * 128), so that its factor's two roundings count, 2^-23 of 24.5 in
+    # log2 units: 2^-18 of a weight; the exponential, the sums and the division as in the reference 2^-20; half a step of fp16.
+    bound = tail * 2.0 ** -32 + want * (2.0 ** -18 + 2.0 ** -20 + 2.0 ** -11) + 2.0 ** -25
+    assert ((out - want).abs() <= bound).all()
+
+
 # ---- values and scores of any size -----------------------------------------------------------
 
 @pytest.mark.parametrize("kind", ["single", "several", "chunk", "shared", "shared several"])
