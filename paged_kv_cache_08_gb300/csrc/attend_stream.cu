@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(Smem<NT, kW>::kThreads, 1)
                     float m = fmaxf(x[nt][c], x[nt][c + 2]);
 #pragma unroll
                     for (int k = 4; k < 32; k <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, k));
-                    m = fmaxf(__fadd_ru(m, -kTopNew), base[nt][c]);   // never below: P must stay in range
+                    // (a column's own scores alone decide: another row may see tokens that this one does not)
+                    m = m - base[nt][c] > kTopMost ? __fadd_ru(m, -kTopNew) : base[nt][c];
                     const float f = join_factor(base[nt][c], m);
                     base[nt][c] = m;
                     sum[nt][c] *= f;

@@ -195,3 +195,36 @@ def test_values_of_any_size(kind, cap, size, rise):
             src, dst = int(case["prefix_tables"][0, 15]), int(case["tables"][s, 15])
             case["v_cache"][dst, :, :n] = case["v_cache"][src, :, :n]
     check_copies(case)
+
+
+# ---- what a row does not see -----------------------------------------------------------------
+
+OPTIONS = [dict(), dict(cap=9.0), dict(biased=True), dict(cap=9.0, biased=True), dict(scale=3e4), dict(scale=3e4, cap=3e5)]
+
+
+def with_options(case, cap=0.0, biased=False, scale=None):
+    case["cap"] = cap
+    if biased:
+        case["slopes"] = slopes_of(case["q"].shape[1])
+    if scale is not None:
+        case["scale"] = scale
+    return case
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("new,options", [(n, o) for n in ([8, 5], [16, 9]) for o in (0, 2, 4)])
+@pytest.mark.parametrize("times", [3.0, -40.0])
+def test_what_later_rows_see_changes_no_bit_of_earlier_ones(dtype, new, options, times):
+    """The newest token of each sequence, which its last row alone sees, with larger scores."""
+    case = with_options(make([150, 77], new, Hq=4, Hkv=2, block=32, dtype=dtype, seed=12), **OPTIONS[options])
+    want = run(case)
+    for s, L in enumerate([150, 77]):
+        at = (int(case["tables"][s, (L - 1) // 32]), slice(None), (L - 1) % 32)
+        case["k_cache"][at] *= times
+        case["v_cache"][at] *= times
+    got = run(case)
+    last = torch.tensor([new[0] - 1, sum(new) - 1])
+    others = torch.ones(sum(new), dtype=torch.bool)
+    others[last] = False
+    assert torch.equal(got[others.to(DEV)], want[others.to(DEV)])
+    assert not torch.equal(got[last.to(DEV)], want[last.to(DEV)])
