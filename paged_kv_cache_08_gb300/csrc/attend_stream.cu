@@ -438,17 +438,14 @@ __global__ void __launch_bounds__(Smem<NT, kW>::kThreads, 1)
                     far |= !(fabsf(x[nt][c]) <= kTanhReach);
                 }
             far = __any_sync(kAll, far);
+            // (a score's own size chooses its form; the vote spares the exponentials where no lane wants one)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const float z = x[nt][c];
-                    if (far) {
-                        x[nt][c] = 1.f - __fdividef(2.f, 1.f + ex2(z * (2.f * kLog2e)));
-                    } else {
-                        const float z2 = z * z;
-                        x[nt][c] = fmaf(fmaf(fmaf(fmaf(kTanh4, z2, kTanh3), z2, kTanh2), z2, kTanh1), z2 * z, z);
-                    }
+                    const float z = x[nt][c], z2 = z * z;
+                    x[nt][c] = fmaf(fmaf(fmaf(fmaf(kTanh4, z2, kTanh3), z2, kTanh2), z2, kTanh1), z2 * z, z);
+                    if (far && !(fabsf(z) <= kTanhReach)) x[nt][c] = 1.f - __fdividef(2.f, 1.f + ex2(z * (2.f * kLog2e)));
                 }
         }
 #pragma unroll

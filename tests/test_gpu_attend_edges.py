@@ -212,7 +212,7 @@ def with_options(case, cap=0.0, biased=False, scale=None):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
-@pytest.mark.parametrize("new,options", [(n, o) for n in ([8, 5], [16, 9]) for o in (0, 2, 4)])
+@pytest.mark.parametrize("new,options", [(n, o) for n in ([8, 5], [16, 9]) for o in range(len(OPTIONS))])
 @pytest.mark.parametrize("times", [3.0, -40.0])
 def test_what_later_rows_see_changes_no_bit_of_earlier_ones(dtype, new, options, times):
     """The newest token of each sequence, which its last row alone sees, with larger scores."""
@@ -228,3 +228,25 @@ def test_what_later_rows_see_changes_no_bit_of_earlier_ones(dtype, new, options,
     others[last] = False
     assert torch.equal(got[others.to(DEV)], want[others.to(DEV)])
     assert not torch.equal(got[last.to(DEV)], want[last.to(DEV)])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("new", [None, [3, 2], [8, 5]])
+@pytest.mark.parametrize("options", range(len(OPTIONS)))
+def test_garbage_nobody_sees_changes_no_bit(dtype, new, options):
+    """Anything behind the context, before the window, in unused blocks: the same bits."""
+    case = with_options(make([150, 77], new, Hq=4, Hkv=2, block=32, dtype=dtype, seed=11), **OPTIONS[options])
+    case["first"] = torch.full((case["q"].shape[0],), 40, dtype=torch.int32)
+    want = run(case)
+    used = torch.zeros(case["k_cache"].shape[0], 32, dtype=torch.bool)
+    for s, L in enumerate([150, 77]):
+        t = torch.arange(40, L)
+        used[case["tables"][s].long()[t // 32], t % 32] = True
+    free = ~used
+    for bad in (math.nan, math.inf, -math.inf, 60000.0, -300.0, 0.0):
+        for cache in ("k_cache", "v_cache"):
+            x = case[cache].permute(0, 2, 1, 3).clone()
+            x[free] = bad
+            case[cache] = x.permute(0, 2, 1, 3).contiguous()
+        assert torch.equal(run(case), want), bad
+    assert all(torch.equal(run(case), want) for _ in range(5))
