@@ -78,6 +78,9 @@ template <typename T>
 __host__ __device__ constexpr float top_new() { return std::is_same<T, __half>::value ? 7.f : -40.f; }
 template <typename T>
 __host__ __device__ constexpr float top_most() { return std::is_same<T, __half>::value ? 15.9f : 8.f; }
+// Scores (in log2 units) beyond which a stage's are rounded before the base is taken from them: from about 2^28 on the
+// rounding of a maximum alone, which the exponents' FMA does not share, would put weights out of fp16's range.
+constexpr float kLargeScore = 0x1p18f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -674,7 +677,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const float xs = a.scale == 0.f ? 1.f : scale * kLog2e, capl = a.cap * kLog2e;
         const float c1 = kTanh1 * ks * k2 * capl, c2 = kTanh2 * ks * k2 * k2 * capl, c3 = kTanh3 * ks * k2 * k2 * k2 * capl,
                     c4 = kTanh4 * ks * k2 * k2 * k2 * k2 * capl;
-        const float reach = !kCap || ks > 1e3f ? 0.f : ks < 1e-4f ? (ks == 0.f ? INFINITY : 0.f) : kTanhReach / ks;
+        const float reach = !kCap || ks > 1e3f ? 0.f : ks < 1e-4f ? (ks == 0.f ? INFINITY : 0.f)
+                                                                  : fminf(kTanhReach, kLargeScore / capl) / ks;
         auto capped2 = [&](float2 s) {   // the factor of S
             const float2 s2 = ffma2(s, s, make_float2(0.f, 0.f));
             float2 q = ffma2(make_float2(c4, c4), s2, make_float2(c3, c3));
@@ -765,7 +769,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
             };
             if (kBias) {
                 const float far = (float)(t0 - pos);
-                const bool before = __all_sync(kAll, t0 + 63 <= pos || !row_ok);   // no key lies behind its row
+                // no key lies behind its row, and the bias can be taken apart
+                const bool before = __all_sync(kAll, (t0 + 63 <= pos && fabsf(slope * far) <= kLargeScore) || !row_ok);
                 if (before && (!kCap || poly)) {
                     bias0 = slope * far;
                     bias8 = 8.f * slope;
@@ -811,20 +816,17 @@ __global__ void __launch_bounds__(kTThreads, 1)
             }
             if (!kBias && !ready && mx != -INFINITY) mx *= kCap ? capped2(make_float2(mx, mx)).x : f;
             // The base moves when a score would put its weight above 2^top_most (the distance is compared, and a new base
-            // rounded up: scores of 2^24 and more leave few bits for such offsets).
+            // rounded towards the maximum: scores of 2^24 and more leave few bits for such offsets).
             const bool move = mx - m_run > top_most<T>();
-            if (__any_sync(kAll, move)) {
-                if (!kBias && !ready && __any_sync(kAll, fabsf(mx) > 0x1p18f && mx != -INFINITY)) {
-                    // scores so large that the maximum's own rounding would count in the exponents
-                    convert();
-                    if (kCap && !whole) {
+            const bool large = (kBias || !kCap) && fabsf(mx) > kLargeScore && mx != -INFINITY;   // (capped ones: `reach`)
+            if (__any_sync(kAll, move || large)) {
+                if (large) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) x[c] = vis[c >> 5] & (1u << (c & 31)) ? x[c] : -INFINITY;
-                    }
-                    ready = kCap;
+                    for (int c = 0; c < 64; ++c) x[c] = kBias ? x[c] + fmaf(bias8, (float)(c >> 3), bias0) : x[c] * f;
+                    bias0 = bias8 = 0.f;
                     f = 1.f;
                 }
-                const float m_new = move ? __fadd_ru(mx, -top_new<T>()) : m_run;
+                const float m_new = !move ? m_run : top_new<T>() > 0.f ? __fadd_ru(mx, -top_new<T>()) : __fadd_rd(mx, -top_new<T>());
                 if (__any_sync(kAll, move && k > 0 && m_run != -INFINITY)) {
                     // O holds the stages before this one once their last product is complete
                     if (!warp_wait(t_pv_done + ((k - 1) & 1) * 8, (uint32_t)((k - 1) >> 1) & 1u)) {

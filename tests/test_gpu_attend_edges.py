@@ -196,6 +196,59 @@ def test_values_of_any_size(kind, cap, size, rise):
             case["v_cache"][dst, :, :n] = case["v_cache"][src, :, :n]
     check_copies(case)
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("kind", ["single", "several", "chunk", "shared", "biased", "biased backwards", "capped"])
+@pytest.mark.parametrize("scale", [1.0, 1e4, 1e8, 1e12])
+def test_scores_of_any_size_row_by_row(dtype, kind, scale):
+    """The token with the largest score wins each row where it leads by more than fp32 can lose; elsewhere the result lies
+    between the smallest and the largest value."""
+    new = {"several": [2, 3], "single": None, "shared": None}.get(kind, [64, 40])
+    case = make([700, 333], new, Hq=2, Hkv=2, dtype=dtype, seed=5, size=100.0, groups=[(0, 2, 300)] if kind == "shared" else None)
+    case["scale"] = scale
+    if "biased" in kind:
+        case["slopes"] = torch.tensor([scale, 0.01 * scale]) * (1 if kind == "biased" else -1)
+    if kind == "capped":
+        case["cap"] = scale * 500
+    n = 80
+    outs = run(copies(case, n)).reshape(n, *case["q"].shape).cpu().double()
+    assert torch.isfinite(outs).all()
+    slopes, cap = case.get("slopes"), case.get("cap") or 0.0
+    # The winner's weight is rounded for its product (2^-11, bf16 2^-16) and not in the sum; the rest is 700 e^-30; the sums
+    # and the division 2^-20; half a step of the result (2^-11, bf16 2^-8).
+    rel = 2.0 ** -10 + 2.0 ** -19 if dtype == F16 else 2.0 ** -8 + 2.0 ** -15
+    won = 0
+    for s in range(2):
+        r0, n_new, L = ref.rows_of(case, s)
+        t = torch.arange(L)
+        blk = case["tables"][s].long()[t // 16]
+        p = torch.arange(L - n_new, L)
+        for h in range(2):
+            K, V = case["k_cache"][blk, h, t % 16].double(), case["v_cache"][blk, h, t % 16].double()
+            Q = case["q"][r0:r0 + n_new, h].double()
+            z = Q @ K.T * scale
+            e = 2.0 ** -16 * (Q.abs() @ K.abs().T) * scale + 2.0 ** -21 * z.abs()      # as in attend_reference.py
+            if cap:
+                z = cap * torch.tanh(z / cap)
+                e = e + 2.0 ** -21 * cap
+            if slopes is not None:
+                bias = slopes[h].double() * (p[:, None] - t)
+                z, e = z - bias, e + 2.0 ** -21 * bias.abs()
+            seen = t <= p[:, None]
+            best = torch.where(seen, z, -math.inf).argmax(-1, keepdim=True)
+            behind = (z - e).gather(-1, best) - (z + e)
+            lead = torch.where(seen & (t != best), behind, math.inf).amin(-1)
+            for out in (outs[0], outs[n // 2], outs[-1]):
+                o = out[r0:r0 + n_new, h]
+                lo = torch.where(seen[..., None], V, math.inf).amin(1)
+                hi = torch.where(seen[..., None], V, -math.inf).amax(1)
+                slack = rel * torch.maximum(lo.abs(), hi.abs())
+                assert ((o >= lo - slack) & (o <= hi + slack)).all()
+                sure = lead > 30
+                won += int(sure.sum())
+                want = V[best[:, 0]]
+                assert ((o - want).abs() <= rel * want.abs() + 2.0 ** -25)[sure].all()
+    assert won > 0 or kind == "capped" or "biased" in kind
+
 
 # ---- what a row does not see -----------------------------------------------------------------
 
