@@ -21,8 +21,8 @@
 // warp 11 looks through V in stages that some row does not see whole and puts zero in such places and in rows of blocks
 // outside the pool; a row that does see a non-finite value takes it at its end, from memory.
 //
-// Caps: tanh is a polynomial on the FMA units while every score of a warp's stage stays within 3/4 of the cap, else
-// 1 - 2 / (1 + e^2y) on the special-function unit, which the softmax's own exponentials already fill.
+// Caps: tanh is a polynomial on the FMA units for scores within 3/4 of the cap, else 1 - 2 / (1 + e^2y) on the
+// special-function unit, which the softmax's own exponentials already fill.
 // P is rounded to fp16, or taken as a high and a low bf16 part (two products): 8 bits of a weight would be the largest error
 // of the result.
 //
@@ -96,12 +96,6 @@ struct TcLaunch {
     int slot0;
     int R_log2;      // log2 of a box's rows
 };
-
-__device__ __forceinline__ float fmin3(float a, float b, float c) {
-    float r;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
@@ -641,7 +635,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         // whole rows of memory (when all products with Q are done)
         const uint32_t warp_rows = base + kOffQ + t * kQTile + (warp & 3) * 32 * 128;
         auto row_chunk = [&](int r, int c) { return warp_rows + (c >> 3) * kQHalf + r * 128 + (((c ^ r) & 7) << 4); };
-                const uint32_t t_s_full = s_full + t * 8;
+        const uint32_t t_s_full = s_full + t * 8;
         const uint32_t t_p_full = p_full + t * 16;
         const uint32_t t_pv_done = pv_done + t * 16;
         {
@@ -672,20 +666,18 @@ __global__ void __launch_bounds__(kTThreads, 1)
         auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {
             return __all_sync(kAll, bar_wait(bar, parity));
         };
-        // log2(e) times the score: xs * S, or capped (while |S| <= reach) S * (c0 + c1 S^2 + .. + c4 S^8)
-        const float scale = fabsf(a.scale), ks = kCap ? scale / a.cap : 0.f, k2 = ks * ks;
-        const float xs = a.scale == 0.f ? 1.f : scale * kLog2e, capl = a.cap * kLog2e;
-        const float c1 = kTanh1 * ks * k2 * capl, c2 = kTanh2 * ks * k2 * k2 * capl, c3 = kTanh3 * ks * k2 * k2 * k2 * capl,
-                    c4 = kTanh4 * ks * k2 * k2 * k2 * k2 * capl;
-        const float reach = !kCap || ks > 1e3f ? 0.f : ks < 1e-4f ? (ks == 0.f ? INFINITY : 0.f)
-                                                                  : fminf(kTanhReach, kLargeScore / capl) / ks;
-        auto capped2 = [&](float2 s) {   // the factor of S
-            const float2 s2 = ffma2(s, s, make_float2(0.f, 0.f));
-            float2 q = ffma2(make_float2(c4, c4), s2, make_float2(c3, c3));
-            q = ffma2(q, s2, make_float2(c2, c2));
-            q = ffma2(q, s2, make_float2(c1, c1));
-            return ffma2(q, s2, make_float2(xs, xs));
+        // log2(e) times the score: xs * S, or with a cap capl tanh(y), y = ks S (while |y| <= kTanhReach a polynomial)
+        const float scale = fabsf(a.scale), ks = kCap ? scale / a.cap : 0.f, xs = a.scale == 0.f ? 1.f : scale * kLog2e;
+        const float capl = a.cap * kLog2e, c1 = kTanh1 * capl, c2 = kTanh2 * capl, c3 = kTanh3 * capl, c4 = kTanh4 * capl;
+        auto capped2 = [&](float2 y) {
+            const float2 y2 = ffma2(y, y, make_float2(0.f, 0.f));
+            float2 q = ffma2(make_float2(c4, c4), y2, make_float2(c3, c3));
+            q = ffma2(q, y2, make_float2(c2, c2));
+            q = ffma2(q, y2, make_float2(c1, c1));
+            q = ffma2(q, y2, make_float2(capl, capl));
+            return ffma2(y, q, make_float2(0.f, 0.f));
         };
+        auto capped_far = [&](float y) { return capl - __fdividef(2.f * capl, 1.f + ex2(y * (2.f * kLog2e))); };
         float2 step2[kBias ? 4 : 1];     // the bias of eight keys from the first one's on
         if (kBias)
 #pragma unroll
@@ -719,106 +711,74 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     vis[e] = (uint32_t)(there >> (32 * e)) & ~behind & ~before;
                 }
             }
-            bool poly = kCap;   // the polynomial holds for all of the warp's scores
-            float u = 0.f, raw = 0.f;
+            // A cap: log2 units in the place of S.  A score's own size chooses the form of its tanh, so that nothing else can
+            // change its bits; the vote spares the exponentials where no score of the warp's stage wants one.
             if (kCap) {
-                // (a NaN is passed over by the extremes and goes through the polynomial as it is)
-                float lo4[4], hi4[4];
+                float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    lo4[e] = fmin3(x[e], x[e + 4], x[e + 8]);
-                    hi4[e] = fmax3(x[e], x[e + 4], x[e + 8]);
-#pragma unroll
-                    for (int c = e + 12; c + 4 < 64; c += 8) {
-                        lo4[e] = fmin3(lo4[e], x[c], x[c + 4]);
-                        hi4[e] = fmax3(hi4[e], x[c], x[c + 4]);
-                    }
-                    lo4[e] = fminf(lo4[e], x[e + 60]);
-                    hi4[e] = fmaxf(hi4[e], x[e + 60]);
+                for (int c = 0; c < 64; c += 2) {
+                    const float2 y = ffma2(make_float2(x[c], x[c + 1]), make_float2(ks, ks), make_float2(0.f, 0.f));
+                    x[c] = y.x;
+                    x[c + 1] = y.y;
+                    m4[c >> 1 & 3] = fmax3(m4[c >> 1 & 3], fabsf(y.x), fabsf(y.y));
                 }
-                raw = fmaxf(fmax3(hi4[0], hi4[1], hi4[2]), hi4[3]);
-                u = fmaxf(fabsf(raw), fabsf(fminf(fmin3(lo4[0], lo4[1], lo4[2]), lo4[3])));
-                poly = __all_sync(kAll, u <= reach);
-            }
-            // What the registers hold: S where its factor can wait for the exponent's FMA, else log2 units (`ready`), with a
-            // bias that lacks `bias0` and `bias8` times the group of eight keys.
-            bool ready = kBias || (kCap && !poly);
-            float f = kBias ? 1.f : xs;   // (without a cap: the factor still to apply)
-            float bias0 = 0.f, bias8 = 0.f;
-            auto convert = [&]() {
-                if (kCap && !poly && __all_sync(kAll, u * ks <= kTanhReach)) {
-                    // (a cap whose powers leave fp32's range)
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        const float y = x[c] * ks, y2 = y * y;
-                        x[c] = capl * fmaf(fmaf(fmaf(fmaf(kTanh4, y2, kTanh3), y2, kTanh2), y2, kTanh1), y2 * y, y);
-                    }
-                } else if (kCap && !poly) {
-                    const float e2 = 2.f * kLog2e * ks;
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) x[c] = capl - __fdividef(2.f * capl, 1.f + ex2(x[c] * e2));
-                } else if (!kBias || kCap) {
+                if (__any_sync(kAll, fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) > kTanhReach)) {
 #pragma unroll
                     for (int c = 0; c < 64; c += 2) {
-                        const float2 s = make_float2(x[c], x[c + 1]);
-                        const float2 y = ffma2(s, kCap ? capped2(s) : make_float2(xs, xs), make_float2(0.f, 0.f));
-                        x[c] = y.x;
-                        x[c + 1] = y.y;
+                        const float2 y = make_float2(x[c], x[c + 1]), z = capped2(y);
+                        const float e0 = capped_far(y.x), e1 = capped_far(y.y);
+                        x[c] = fabsf(y.x) > kTanhReach ? e0 : z.x;
+                        x[c + 1] = fabsf(y.y) > kTanhReach ? e1 : z.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) {
+                        const float2 z = capped2(make_float2(x[c], x[c + 1]));
+                        x[c] = z.x;
+                        x[c + 1] = z.y;
                     }
                 }
-            };
+            }
+            float f = kBias || kCap ? 1.f : xs;   // the factor still to apply
+            float bias0 = 0.f, bias8 = 0.f;       // what the registers lack of the bias: bias0, and bias8 times the group of eight keys
             if (kBias) {
-                const float far = (float)(t0 - pos);
+                const float far = (float)(t0 - pos), to_log2 = kCap ? 1.f : xs;
                 // no key lies behind its row, and the bias can be taken apart
                 const bool before = __all_sync(kAll, (t0 + 63 <= pos && fabsf(slope * far) <= kLargeScore) || !row_ok);
-                if (before && (!kCap || poly)) {
+                if (before) {
                     bias0 = slope * far;
                     bias8 = 8.f * slope;
 #pragma unroll
                     for (int c = 0; c < 64; c += 2) {
-                        const float2 s = make_float2(x[c], x[c + 1]);
-                        const float2 y = ffma2(s, kCap ? capped2(s) : make_float2(xs, xs), step2[kBias ? (c >> 1 & 3) : 0]);
+                        const float2 y = ffma2(make_float2(x[c], x[c + 1]), make_float2(to_log2, to_log2), step2[kBias ? (c >> 1 & 3) : 0]);
                         x[c] = y.x;
                         x[c + 1] = y.y;
                     }
                 } else {
-                    convert();
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) x[c] = fmaf(x[c], kCap ? 1.f : xs, -slope * fabsf(far + (float)c));
+                    for (int c = 0; c < 64; ++c) x[c] = fmaf(x[c], to_log2, -slope * fabsf(far + (float)c));
                 }
-            } else if (ready) {
-                convert();
             }
-            if (!whole && (!kCap || ready)) {
+            if (!whole) {
 #pragma unroll
                 for (int c = 0; c < 64; ++c) x[c] = vis[c >> 5] & (1u << (c & 31)) ? x[c] : -INFINITY;
-            } else if (!whole) {   // (S is still to go through the polynomial: its maximum over what is seen)
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < 64; c += 2)
-                    m4[c >> 1 & 3] = fmax3(m4[c >> 1 & 3], vis[c >> 5] & (1u << (c & 31)) ? x[c] : -INFINITY,
-                                           vis[c >> 5] & (2u << (c & 31)) ? x[c + 1] : -INFINITY);
-                raw = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
             }
             // the maximum by groups of eight, as trees of three-input steps
-            float mx = raw;
-            if (!kCap || ready) {
-                float m8[8];
+            float m8[8];
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    float m = fmax3(x[8 * g], x[8 * g + 1], x[8 * g + 2]);
-                    m = fmax3(m, x[8 * g + 3], x[8 * g + 4]);
-                    m = fmax3(m, x[8 * g + 5], x[8 * g + 6]);
-                    m8[g] = fmaxf(m, x[8 * g + 7]);
-                    if (kBias) m8[g] += fmaf(bias8, (float)g, bias0);
-                }
-                mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+            for (int g = 0; g < 8; ++g) {
+                float m = fmax3(x[8 * g], x[8 * g + 1], x[8 * g + 2]);
+                m = fmax3(m, x[8 * g + 3], x[8 * g + 4]);
+                m = fmax3(m, x[8 * g + 5], x[8 * g + 6]);
+                m8[g] = fmaxf(m, x[8 * g + 7]);
+                if (kBias) m8[g] += fmaf(bias8, (float)g, bias0);
             }
-            if (!kBias && !ready && mx != -INFINITY) mx *= kCap ? capped2(make_float2(mx, mx)).x : f;
+            float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+            if (!kBias && !kCap && mx != -INFINITY) mx *= f;
             // The base moves when a score would put its weight above 2^top_most (the distance is compared, and a new base
             // rounded towards the maximum: scores of 2^24 and more leave few bits for such offsets).
             const bool move = mx - m_run > top_most<T>();
-            const bool large = (kBias || !kCap) && fabsf(mx) > kLargeScore && mx != -INFINITY;   // (capped ones: `reach`)
+            const bool large = (kBias || !kCap) && fabsf(mx) > kLargeScore && mx != -INFINITY;   // (capped ones are rounded)
             if (__any_sync(kAll, move || large)) {
                 if (large) {
 #pragma unroll
@@ -857,7 +817,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             constexpr int kPart = kSplitP ? 16 : 32;
             const uint32_t p_at = lane_addr + kColP + (kSplitP ? 0u : (uint32_t)(k & 1) * 32u);
             uint32_t w[kPart];
-            auto weights = [&](auto exponent, auto masked) {
+            auto weights = [&](auto exponent) {
 #pragma unroll
                 for (int part = 0; part < 32; part += kPart) {
                     uint32_t low[kPart];
@@ -865,12 +825,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     for (int c = 0; c < kPart; ++c) {
                         const int c2 = part + c;
                         const float2 e2 = exponent(c2, make_float2(x[2 * c2], x[2 * c2 + 1]));
-                        float p0 = ex2(e2.x);
-                        float p1 = ex2(e2.y);
-                        if (decltype(masked)::value) {
-                            p0 = vis[c2 >> 4] & (1u << (2 * c2 & 31)) ? p0 : 0.f;
-                            p1 = vis[c2 >> 4] & (2u << (2 * c2 & 31)) ? p1 : 0.f;
-                        }
+                        const float p0 = ex2(e2.x), p1 = ex2(e2.y);
                         w[c] = Elem<T>::pack2(p0, p1);
                         if (kSplitP) {
                             const float2 d = fadd2(make_float2(p0, p1), Elem<T>::to_float2(w[c] ^ 0x80008000u));   // p - w
@@ -893,15 +848,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 float2 from[8];   // the base less what the bias of a group lacks
 #pragma unroll
                 for (int g = 0; g < 8; ++g) from[g].x = from[g].y = fmaf(bias8, (float)g, bias0) - m_use;
-                weights([&](int c2, float2 y) { return fadd2(y, from[c2 >> 2]); }, std::false_type{});
+                weights([&](int c2, float2 y) { return fadd2(y, from[c2 >> 2]); });
             } else if (!kCap) {
-                weights([&](int, float2 s) { return ffma2(s, make_float2(f, f), nm2); }, std::false_type{});
-            } else if (ready) {
-                weights([&](int, float2 y) { return fadd2(y, nm2); }, std::false_type{});
-            } else if (whole) {
-                weights([&](int, float2 s) { return ffma2(s, capped2(s), nm2); }, std::false_type{});
+                weights([&](int, float2 s) { return ffma2(s, make_float2(f, f), nm2); });
             } else {
-                weights([&](int, float2 s) { return ffma2(s, capped2(s), nm2); }, std::true_type{});
+                weights([&](int, float2 y) { return fadd2(y, nm2); });
             }
             if (kSplitP && dead) break;
             if constexpr (!kSplitP) tmem_st32u(p_at, w);

@@ -265,7 +265,7 @@ def with_options(case, cap=0.0, biased=False, scale=None):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
-@pytest.mark.parametrize("new,options", [(n, o) for n in ([8, 5], [16, 9]) for o in range(len(OPTIONS))])
+@pytest.mark.parametrize("new,options", [(n, o) for n in ([8, 5], [16, 9], [70, 40]) for o in range(len(OPTIONS))])
 @pytest.mark.parametrize("times", [3.0, -40.0])
 def test_what_later_rows_see_changes_no_bit_of_earlier_ones(dtype, new, options, times):
     """The newest token of each sequence, which its last row alone sees, with larger scores."""
@@ -284,7 +284,7 @@ def test_what_later_rows_see_changes_no_bit_of_earlier_ones(dtype, new, options,
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
-@pytest.mark.parametrize("new", [None, [3, 2], [8, 5]])
+@pytest.mark.parametrize("new", [None, [3, 2], [8, 5], [70, 40]])
 @pytest.mark.parametrize("options", range(len(OPTIONS)))
 def test_garbage_nobody_sees_changes_no_bit(dtype, new, options):
     """Anything behind the context, before the window, in unused blocks: the same bits."""
@@ -303,3 +303,21 @@ def test_garbage_nobody_sees_changes_no_bit(dtype, new, options):
             case[cache] = x.permute(0, 2, 1, 3).contiguous()
         assert torch.equal(run(case), want), bad
     assert all(torch.equal(run(case), want) for _ in range(5))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_garbage_behind_shared_prefixes_changes_no_bit(dtype):
+    case = make([150, 77, 300], Hq=12, Hkv=2, block=32, dtype=dtype, seed=13, groups=[(0, 3, 70)])
+    want = run(case)
+    used = torch.zeros(case["k_cache"].shape[0], 32, dtype=torch.bool)
+    for s, L in enumerate([150, 77, 300]):
+        t = torch.arange(L)
+        used[case["tables"][s].long()[t // 32], t % 32] = True
+    t = torch.arange(70)
+    used[case["prefix_tables"][0].long()[t // 32], t % 32] = True
+    for bad in (math.nan, math.inf, 60000.0, 0.0):
+        for cache in ("k_cache", "v_cache"):
+            x = case[cache].permute(0, 2, 1, 3).clone()
+            x[~used] = bad
+            case[cache] = x.permute(0, 2, 1, 3).contiguous()
+        assert torch.equal(run(case), want), bad
