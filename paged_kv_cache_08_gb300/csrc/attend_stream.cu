@@ -518,12 +518,8 @@ __global__ void __launch_bounds__(Smem<NT, kW>::kThreads, 1)
         for (int nt = 0; nt < NT; ++nt) {
             float pr[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) pr[c] = ex2(x[nt][c] - base[nt][c & 1]);
-            if (masked) {   // a row without a base yet has -inf - -inf here
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (!sees(nt, c & 1, t0 + g + (c >> 1) * 8)) pr[c] = 0.f;
-            }
+            for (int c = 0; c < 4; ++c)   // (0 for what a row without a base yet has: masked scores and ones below fp32's range)
+                pr[c] = ex2(x[nt][c] - (base[nt][c & 1] == -INFINITY ? 0.f : base[nt][c & 1]));
             sum[nt][0] += pr[0] + pr[2];
             sum[nt][1] += pr[1] + pr[3];
             const uint32_t h0 = Elem<T>::pack2(pr[0], pr[1]), h1 = Elem<T>::pack2(pr[2], pr[3]);

@@ -250,6 +250,25 @@ def test_scores_of_any_size_row_by_row(dtype, kind, scale):
     assert won > 0 or kind == "capped" or "biased" in kind
 
 
+@pytest.mark.parametrize("new", [None, [3, 2], [50, 40]])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("shared", [False, True])
+def test_keys_of_the_types_lowest_value(new, cap, shared):
+    """Scores below fp32's range (here -4e40, of the first 40 tokens) leave no weight."""
+    if shared and cap:
+        return
+    case = make([150, 77], new, Hq=4, Hkv=2, dtype=BF16, seed=21, groups=[(0, 2, 45)] if shared else None)
+    case["cap"] = cap
+    case["q"] = case["q"].abs() + 0.5
+    lowest = torch.finfo(BF16).min
+    for s in range(2):
+        t = torch.arange(40)
+        case["k_cache"][case["tables"][s].long()[t // 16], :, t % 16] = lowest
+    if shared:
+        case["k_cache"][case["prefix_tables"][0].long()[t // 16], :, t % 16] = lowest
+    ref.check(run(case), case)
+
+
 # ---- what a row does not see -----------------------------------------------------------------
 
 OPTIONS = [dict(), dict(cap=9.0), dict(biased=True), dict(cap=9.0, biased=True), dict(scale=3e4), dict(scale=3e4, cap=3e5)]
