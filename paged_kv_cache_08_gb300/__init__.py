@@ -1078,6 +1078,8 @@ def _attend(name, q, k_cache, v_cache, block_tables, context_lens, query_start, 
         cap = float(cap)
         if not 0.0 <= cap < math.inf:
             raise ValueError("cap must be 0 (none) or positive")
+        if cap > 0.0:
+            cap = max(cap, 2.0 ** -126)   # (fp32 would have none)
         sl_ptr = fk_ptr = bi_ptr = None
         if slopes is not None:
             sl_ptr = _want("slopes", slopes, torch.float32, dev)

@@ -97,6 +97,22 @@ Dispatch dispatch(int num_seqs, int num_q_tokens, int max_q, int num_q_heads, in
     return d;
 }
 
+// Caps so far from the scores that the kernels' fp32 would leave its range are put within it.  A cap of 2^-64 or less leaves
+// every score within 2^-64 of zero, whose weights are all one; under one of 2^80 |scale| and more no product below 2^68 is
+// changed by as much as its own rounding.
+void normalise_cap(AttendArgs* a) {
+    if (a->cap == 0.f) return;
+    if (a->cap <= 0x1p-64f) {
+        a->cap = a->scale = 0.f;
+    } else if (a->cap >= 0x1p80 * std::fabs((double)a->scale)) {
+        a->cap = 0.f;
+    } else {
+        a->cap = std::fmin(a->cap, 0x1p120f);
+        const double most = 0x1p90 * a->cap;   // (scores of other than zero are +-cap)
+        if (std::fabs(a->scale) > most) a->scale = std::copysign((float)most, a->scale);
+    }
+}
+
 int run(AttendArgs a, int head_dim, int dtype, void* workspace, size_t workspace_bytes, void* stream_ptr) {
     if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_INVALID_ARG;
     const int rc = check_shape(a.num_seqs, a.q_rows, a.max_q, a.num_q_heads, a.num_kv_heads, head_dim, a.block_size,
@@ -115,6 +131,7 @@ int run(AttendArgs a, int head_dim, int dtype, void* workspace, size_t workspace
     const cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     char* ws = static_cast<char*>(workspace);
     a.status = device_status_ptr();
+    normalise_cap(&a);
     if (d.partial) {
         a.part_o = reinterpret_cast<float*>(ws + d.o);
         a.part_ml = reinterpret_cast<float2*>(ws + d.ml);

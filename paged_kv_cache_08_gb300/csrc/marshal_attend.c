@@ -108,13 +108,15 @@ static PyObject *attend(PyObject *self, PyObject *const *a, Py_ssize_t nargs) {
         Py_RETURN_NONE;
     for (int i = 0; i < 4; ++i)
         if (nc[i] != nv[i]) Py_RETURN_NONE;
-    const double scale = PyFloat_AsDouble(a[6]), cap = shared ? 0.0 : PyFloat_AsDouble(a[10]);
+    const double scale = PyFloat_AsDouble(a[6]);
+    double cap = shared ? 0.0 : PyFloat_AsDouble(a[10]);
     const long long hkv = PyLong_AsLongLong(a[7]), max_q = PyLong_AsLongLong(a[8]);
     if (PyErr_Occurred()) {
         PyErr_Clear();
         Py_RETURN_NONE;
     }
     if (hkv != nc[1] || nq[2] != nc[3] || (!t.qs && nq[0] != t.S) || max_q < 1 || max_q > 0x7fffffffLL) Py_RETURN_NONE;
+    if (cap > 0.0 && cap < 0x1p-126) cap = 0x1p-126; /* (fp32 would have none) */
     float *slopes = NULL;
     int32_t *first = NULL, *bidirectional = NULL, *pt = NULL, *pl = NULL, *gs = NULL;
     if (shared) {

@@ -269,6 +269,22 @@ def test_keys_of_the_types_lowest_value(new, cap, shared):
     ref.check(run(case), case)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("new", [None, [3, 2], [50, 40]])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("cap", [1e-300, 1e-40, 1e-30, 1e-6, 1e6, 1e20, 3e38])
+def test_caps_of_any_size(dtype, new, biased, cap):
+    """A tiny cap leaves all scores alike, a huge one changes none."""
+    case = make([150, 77], new, Hq=4, Hkv=2, dtype=dtype, seed=22)
+    case["q"][0, 0] = 0                      # scores of exactly zero, too
+    case["cap"] = cap
+    if biased:
+        case["slopes"] = slopes_of(4)
+    out = run(case)
+    # the bound's 2^-21 of the cap is what the exponential may lose; at such sizes the cap changes nothing
+    ref.check(out, dict(case, cap=cap if cap < 1e4 else 0.0))
+
+
 # ---- what a row does not see -----------------------------------------------------------------
 
 OPTIONS = [dict(), dict(cap=9.0), dict(biased=True), dict(cap=9.0, biased=True), dict(scale=3e4), dict(scale=3e4, cap=3e5)]
