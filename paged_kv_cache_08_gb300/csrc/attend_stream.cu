@@ -87,7 +87,8 @@ struct Smem {
     static constexpr uint32_t kOffN = kOffRow0 + kMaxSeqs * 4;
     static constexpr uint32_t kBytes = kOffN + kMaxSeqs;
     static_assert(kRing >= kRows * kHeadDim * 4, "a warp's last piece is kept in its ring");
-    static_assert(1024 + kBytes + 64 <= 227 * 1024, "shared memory of one CTA");
+    static constexpr uint32_t kStatic = kWarps * 8;   // declared in the kernel
+    static_assert(1024 + kBytes + kStatic <= 227 * 1024, "shared memory of one CTA");
 };
 
 // What a warp leaves for the end of its CTA (flags as in q8_join.h, then segments as s << 16 | h).
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(Smem<NT, kW>::kThreads, 1)
     auto segs_of = [&](int s) { return segments(p, n_of[s]); };
     {
         __shared__ long long warp_sum_of[kWarps];
+        static_assert(sizeof(warp_sum_of) == M::kStatic, "as Smem counts it");
         long long carry = 0;
         for (int s0 = 0; s0 < S; s0 += kThreads) {
             const int s = s0 + tid;
