@@ -8,7 +8,7 @@ import torch
 import attend_reference as ref
 import paged_kv_cache_08_gb300 as pa
 from paged_kv_cache_08_gb300 import _native
-from test_gpu_attend import BF16, DEV, F16, clean, make, run, slopes_of, status  # noqa: F401 (status: every test's)
+from test_gpu_attend import BF16, DEV, F16, clean, make, run, slopes_of, status, window  # noqa: F401 (status: every test's)
 
 pytestmark = pytest.mark.gpu
 
@@ -113,6 +113,14 @@ def test_weights_keep_their_bits_in_tiles(call, dtype, cap):
         return split_heads(out, case)
     one, rows = as_single_tokens(case)
     ref.check(out[rows], one)
+
+
+@pytest.mark.parametrize("new", [None, [2, 3]])
+def test_weights_keep_their_bits_where_a_prefix_is_not_shared(new):
+    """Tables so small that the prefix is read for every sequence."""
+    case = make([300, 257], new, Hq=6, Hkv=2, dtype=BF16, seed=47, groups=[(0, 2, 80)], wide=False)
+    one, rows = as_single_tokens(case)
+    ref.check(run(case).cpu()[rows], one)
 
 
 def split_heads(out, case):
@@ -356,3 +364,32 @@ def test_garbage_behind_shared_prefixes_changes_no_bit(dtype):
             x[~used] = bad
             case[cache] = x.permute(0, 2, 1, 3).contiguous()
         assert torch.equal(run(case), want), bad
+
+
+# ---- many query heads a kv head --------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("Hq,Hkv,block", [(40, 1, 16), (66, 2, 64), (300, 1, 128)])
+@pytest.mark.parametrize("cap,biased,span", [(0.0, False, 0), (5.0, True, 0), (0.0, True, 30), (2.0, False, 30)])
+def test_more_than_32_query_heads_a_kv_head(dtype, Hq, Hkv, block, cap, biased, span):
+    """Single tokens in tiles."""
+    case = make([1, 0, 7, 64, 65, 255, 700, 33], Hq=Hq, Hkv=Hkv, block=block, dtype=dtype, seed=Hq)
+    case["cap"] = cap
+    if biased:
+        case["slopes"] = slopes_of(Hq)
+    if span:
+        case["first"] = window(case, span)
+        case["first"][3] = 10**9
+    out = run(case)
+    ref.check(out, case)
+    assert not out[1].any() and (not span or not out[3].any())
+    assert clean() == 0
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("wide", [False, True])
+def test_more_than_32_query_heads_share_a_prefix(dtype, wide):
+    case = make([90, 0, 300, 64, 500, 41], Hq=80, Hkv=2, block=16, dtype=dtype, seed=2, groups=[(0, 2, 64), (2, 5, 130)],
+                wide=wide)
+    ref.check(run(case), case)
+    assert clean() == 0
