@@ -98,6 +98,15 @@ __device__ __forceinline__ NewRows rows_of(const AttendArgs& a, int s, int L) {
 constexpr float kTanhReach = 0.75f;
 constexpr float kTanh1 = -0.333296676f, kTanh2 = 0.132682369f, kTanh3 = -0.0502779472f, kTanh4 = 0.0131058294f;
 
+// Weights as a high and a low bf16 part, 16 bits together.  The high part is rounded towards zero and the low one is at least
+// 2^-22 of the weight, so that both are positive and a value of infinity stays one.
+__device__ __forceinline__ uint32_t high_part2(float a, float b) {
+    uint32_t w;
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    return w;
+}
+constexpr float kLowPart = 1.f + 0x1p-22f;   // low = kLowPart * weight - high
+
 // Which keys a launch of attend_tc.cu reads.
 enum AttendKeys { kAllKeys = 0, kTailKeys = 1, kPrefixKeys = 2 };
 

@@ -524,13 +524,14 @@ __global__ void __launch_bounds__(Smem<NT, kW>::kThreads, 1)
                 pr[c] = ex2(x[nt][c] - (base[nt][c & 1] == -INFINITY ? 0.f : base[nt][c & 1]));
             sum[nt][0] += pr[0] + pr[2];
             sum[nt][1] += pr[1] + pr[3];
-            const uint32_t h0 = Elem<T>::pack2(pr[0], pr[1]), h1 = Elem<T>::pack2(pr[2], pr[3]);
+            const uint32_t h0 = kSplitP ? high_part2(pr[0], pr[1]) : Elem<T>::pack2(pr[0], pr[1]),
+                           h1 = kSplitP ? high_part2(pr[2], pr[3]) : Elem<T>::pack2(pr[2], pr[3]);
             b0[nt] = movmatrix_trans(h0);
             b1[nt] = movmatrix_trans(h1);
             if (kSplitP) {
                 const float2 f0 = Elem<T>::to_float2(h0), f1 = Elem<T>::to_float2(h1);
-                l0[kSplitP ? nt : 0] = movmatrix_trans(Elem<T>::pack2(pr[0] - f0.x, pr[1] - f0.y));
-                l1[kSplitP ? nt : 0] = movmatrix_trans(Elem<T>::pack2(pr[2] - f1.x, pr[3] - f1.y));
+                l0[kSplitP ? nt : 0] = movmatrix_trans(Elem<T>::pack2(fmaf(pr[0], kLowPart, -f0.x), fmaf(pr[1], kLowPart, -f0.y)));
+                l1[kSplitP ? nt : 0] = movmatrix_trans(Elem<T>::pack2(fmaf(pr[2], kLowPart, -f1.x), fmaf(pr[3], kLowPart, -f1.y)));
             }
         }
         // O += V^T P^T

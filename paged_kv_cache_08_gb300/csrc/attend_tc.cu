@@ -826,9 +826,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         const int c2 = part + c;
                         const float2 e2 = exponent(c2, make_float2(x[2 * c2], x[2 * c2 + 1]));
                         const float p0 = ex2(e2.x), p1 = ex2(e2.y);
-                        w[c] = Elem<T>::pack2(p0, p1);
+                        w[c] = kSplitP ? high_part2(p0, p1) : Elem<T>::pack2(p0, p1);
                         if (kSplitP) {
-                            const float2 d = fadd2(make_float2(p0, p1), Elem<T>::to_float2(w[c] ^ 0x80008000u));   // p - w
+                            const float2 d = ffma2(make_float2(p0, p1), make_float2(kLowPart, kLowPart), Elem<T>::to_float2(w[c] ^ 0x80008000u));
                             low[c] = Elem<T>::pack2(d.x, d.y);
                         }
                         rs2[c2 & 3] = fadd2(rs2[c2 & 3], make_float2(p0, p1));

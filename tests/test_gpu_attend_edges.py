@@ -293,6 +293,23 @@ def test_caps_of_any_size(dtype, new, biased, cap):
     ref.check(out, dict(case, cap=cap if cap < 1e4 else 0.0))
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("kind", ["single", "several", "chunk", "shared"])
+@pytest.mark.parametrize("size", [0.3, 2.0])
+def test_infinite_values_that_every_row_sees(dtype, kind, size):
+    """They are infinities of the result, and NaN only where both signs meet or a NaN is among them."""
+    new = dict(several=[3, 2], chunk=[70, 40]).get(kind)
+    case = make([400, 390], new, Hq=4, Hkv=2, block=32, dtype=dtype, seed=31, size=size,
+                groups=[(0, 2, 300)] if kind == "shared" else None)
+    values = ((100, 0, 3, math.inf), (150, 1, 7, -math.inf), (151, 1, 9, math.nan), (170, 0, 11, math.inf), (171, 0, 11, -math.inf))
+    for s in range(2):
+        for at, h, d, x in values:
+            case["v_cache"][int(case["tables"][s, at // 32]), h, at % 32, d] = x
+    out = run(case)
+    ref.check(out, case)
+    assert torch.isinf(out).any() and torch.isnan(out).any()
+
+
 # ---- what a row does not see -----------------------------------------------------------------
 
 OPTIONS = [dict(), dict(cap=9.0), dict(biased=True), dict(cap=9.0, biased=True), dict(scale=3e4), dict(scale=3e4, cap=3e5)]
