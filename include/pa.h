@@ -571,7 +571,9 @@ size_t pa_decode_q8_workspace_size(int num_seqs, int num_q_heads, int num_kv_hea
  * Products and sums in fp32, rounded once into `dtype`; the softmax weights enter the PV product with 11 bits (fp16) or 16
  * (bf16: a high and a low part).  Tokens that a row does not see do not affect it, whatever their K and V hold.  Rows
  * that no sequence owns are neither read nor written.  Tokens of a block whose table entry lies outside the pool are left
- * out of the softmax and set PA_DEV_BAD_BLOCK_ID.  pa_decode_scored: one query row per sequence, at position L - 1; L == 0 gives a zero row.
+ * out of the softmax and set PA_DEV_BAD_BLOCK_ID.  pa_decode_scored: one query row per sequence, at position L - 1; L == 0
+ * gives a zero row.  query_start as in pa_multi_query, counts clamped and flagged as there; where it decreases, rows may be
+ * left unwritten.  The 8-bit cache has no calls of this kind.
  * Kernels: while max_q_per_seq x (num_q_heads / num_kv_heads) <= 32 warps that stream equal shares of all tokens some
  * row sees; beyond that tcgen05 tiles of 128 query rows.  Head size 128, block_size 16/32/64/128, at most 65535
  * sequences and query heads and 32767 kv heads, 2^30 tokens a table row, num_blocks x num_kv_heads x block_size and
@@ -602,11 +604,11 @@ int pa_multi_query_scored(void* out, const void* q, const void* k_cache, const v
  * pa_decode's.  context_lens counts the prefix: a sequence shorter than its group's prefix sees its first L tokens.
  * Sequences in no group are read through their own rows alone.
  *   prefix_tables: int32 [num_groups][max_prefix_blocks]; prefix_lens: int32 [num_groups], any number of tokens (clamped
- *   to the table, setting PA_DEV_BAD_CONTEXT where they are read); group_start: int32 [num_groups + 1], non-decreasing within 0 .. num_seqs
- *   (otherwise PA_DEV_BAD_CONTEXT is set and rows of the groups concerned are unspecified); device memory.
+ *   to the table, setting PA_DEV_BAD_CONTEXT where they are read); group_start: int32 [num_groups + 1], non-decreasing
+ *   within 0 .. num_seqs (otherwise PA_DEV_BAD_CONTEXT is set and rows of sequences in groups are unspecified); device memory.
  * Kernels: the prefixes on tcgen05 tiles of 128 query rows of a group, the rest as pa_multi_query_scored, then a launch
- * that joins the parts.  All else (precision, tokens nobody sees, bad blocks, limits) as pa_multi_query_scored;
- * num_groups at most 65535.
+ * that joins the parts.  All else (precision, tokens nobody sees, bad blocks, limits) as pa_multi_query_scored, but scores
+ * are plain ones: neither cap, slopes nor masks; num_groups at most 65535.
  * workspace: pa_attend_workspace_size(...) bytes, as there.  Returns the codes of pa_decode_scored.
  * ---------------------------------------------------------------------------------- */
 int pa_decode_shared(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,

@@ -65,8 +65,8 @@ Dispatch dispatch(int num_seqs, int num_q_tokens, int max_q, int num_q_heads, in
         if (d.stream) {
             // Both parts run side by side, each on SMs of its own: the split that the model of their times finds best.  A
             // stage takes a CTA with two tiles 1.1 us, a streaming CTA reads 60 KB in 1 us with up to 8 rows a segment and
-            // half of that with more, all together 6 GB/s; half the rest of the tables is taken for the tails' length,
-            // which is not known here.
+            // half of that with more, all together 6 TB/s (6000 KB a microsecond); half the rest of the tables is taken for the
+            // tails' length, which is not known here.
             const TcSplits one = tc_splits(group_rows, num_groups, num_kv_heads, prefix, 1, sms);
             const double stages = (double)one.items * num_kv_heads * (double)(prefix / 64 + 1);
             const bool few = group * max_q <= 8;

@@ -26,13 +26,13 @@
 // P is rounded to fp16, or taken as a high and a low bf16 part (two products): 8 bits of a weight would be the largest error
 // of the result.
 //
-// What bounds it: a CTA's stage of 64 tokens (two tiles) takes 2050 cycles without options, of which its products need
-// 1024 and the shared memory that feeds them about 1540 (Q is read again for every 64 keys, K and V by both tiles); the
-// rest is the softmax's chain, two warps a scheduler.  A cap adds five packed FMAs to every pair of scores (2500 cycles),
-// a bias by distance one and the groups' offsets.  16 sequences with 512 new of 4096 tokens, 32 heads: 460 us without
-// options (1.12 PFLOP/s), 376 us for packed documents of 2048 tokens, capped; prompts of 1025 to 2048 tokens behind an
-// image, 32 heads with a bias: 250 us.  A CTA's start and end take 6 us (unit and intervals, Q, first copies, 64 to 128 KB
-// of results at what one SM stores).
+// What bounds it: a CTA's stage of 64 tokens (two tiles) takes about 2050 cycles in fp16 without options, of which its
+// products need 1024 (bf16 1536, for P's two parts) and the shared memory that feeds them about 1540 (Q is read again for
+// every 64 keys, K and V by both tiles); the rest is the softmax's chain, two warps a scheduler.  A cap adds seven packed
+// operations to every pair of scores, a bias by distance one and the groups' offsets.  16 sequences with 512 new of 4096
+// tokens, 32 heads: 465 us in fp16 without options (1.11 PFLOP/s), 590 in bf16, 609 with a cap, 304 for packed documents of
+// 2048 tokens with one; prompts of 1025 to 2048 tokens behind an image, 32 heads in bf16 with a bias: 286 us.  A CTA's start
+// and end take 6 us (unit and intervals, Q, first copies, 64 to 128 KB of results at what one SM stores).
 #include <atomic>
 
 #include "attend.cuh"

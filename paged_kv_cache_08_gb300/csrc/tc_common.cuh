@@ -143,8 +143,8 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
         : "memory");
 }
 
-// 2^x on the special-function unit (approximate, subnormal results flushed to zero): the
-// softmax weights it produces lie in (0, 2^8], and weights below 2^-126 do not matter.
+// 2^x on the special-function unit (approximate, subnormal results flushed to zero: softmax
+// weights below 2^-126 do not matter, whose largest is 2^-40 at least).
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
